@@ -447,6 +447,66 @@ moe_status_t moe_router_backward(const moe_bf16_t* x, const float* w_router, con
                                  moe_bf16_t* dx, float* dw_router, float* dbias, void* ws, size_t ws_bytes,
                                  cudaStream_t stream);
 
+/* ---- Norms around a block ----
+ * The expert layer takes the place of the dense feed-forward block inside a
+ * transformer backbone that stays as it is (section "From Dense to Sparse"):
+ * what enters it is an RMS norm of the residual stream, what leaves it goes
+ * back to the stream. With the stream r [T][d] (bf16 or fp32, moe_stream_type_t)
+ * and the block's output y [T][d] (bf16):
+ *   in front   xn = r * rstd * w,  rstd[t] = (mean_i r[t][i]^2 + eps)^(-1/2)
+ *   behind     out = alpha * r + g * (y * rstd * w), rstd of y
+ *   and then   xn = out * rstd_next * w_next, rstd_next of out as stored: the
+ *              input of the next block, in the same pass
+ * alpha is the residual scale. The gate g has one row of d values for each
+ * gate_rows consecutive tokens (token t takes row t / gate_rows): gate_rows = T
+ * is one row for all (a learned gate per channel), 1 a row per token, the
+ * length of a sequence a row per sequence. Gains w are fp32 [d], the gate bf16.
+ * Sums are in fp32; out and xn are rounded once. d: a positive multiple of 8,
+ * at most 16384. T = 0 launches nothing (the backward calls then zero dw and
+ * dw_next). Rows that hold infinities or NaN give NaN in those rows only. */
+typedef enum { MOE_STREAM_BF16 = 0, MOE_STREAM_FP32 = 1 } moe_stream_type_t;
+
+/* xn [T][d] bf16 and rstd [T] fp32 of x [T][d] (type `type`). eps >= 0. */
+moe_status_t moe_block_norm_in(const void* x, moe_stream_type_t type, const float* w, int T, int d, float eps,
+                               moe_bf16_t* xn, float* rstd, cudaStream_t stream);
+
+/* out [T][d] (type of r) and rstd [T]; with w_next also xn [T][d] bf16 and
+ * rstd_next [T] (w_next NULL: xn and rstd_next are not read or written, may be
+ * NULL). gate [ceil(T / gate_rows)][d] bf16, or NULL with gate_rows = 0.
+ * out may be the memory of r itself; otherwise no output overlaps an input. */
+moe_status_t moe_block_norm_out(const moe_bf16_t* y, const void* r, moe_stream_type_t type, const float* w,
+                                const moe_bf16_t* gate, int gate_rows, float alpha, const float* w_next, int T, int d,
+                                float eps, void* out, float* rstd, moe_bf16_t* xn, float* rstd_next,
+                                cudaStream_t stream);
+
+/* Bytes of workspace the two backward calls need (gate_rows = 0 for
+ * moe_block_norm_in_backward and without a gate). */
+size_t moe_block_norm_backward_workspace_size(int T, int d, int gate_rows);
+
+/* Gradient of moe_block_norm_in, with the gradient that flows past the block:
+ *   dx = dres + rstd * (dxn w - xhat mean(dxn w xhat)),  xhat = x rstd
+ *   dw = sum_t dxn xhat
+ * dxn [T][d] bf16, dres and dx [T][d] of x's type (dres NULL: none; dx may be
+ * dres), rstd of the forward, dw [d] fp32. Sums over tokens in a fixed order
+ * (no atomics). ws 16-byte aligned, need not be initialised. */
+moe_status_t moe_block_norm_in_backward(const moe_bf16_t* dxn, const void* dres, const void* x, moe_stream_type_t type,
+                                        const float* w, const float* rstd, int T, int d, void* dx, float* dw, void* ws,
+                                        size_t ws_bytes, cudaStream_t stream);
+
+/* Gradient of moe_block_norm_out. With dR the whole gradient of `out` (dout, of
+ * out's type, along the stream; with w_next also dxn [T][d] bf16 through the next norm):
+ *   dR = dout + rstd_next * (dxn w_next - ohat mean(dxn w_next ohat)),  ohat = out rstd_next
+ *   dr = alpha dR,   dy = rstd * (dR g w - yhat mean(dR g w yhat)),  yhat = y rstd
+ *   dw = sum_t dR g yhat,  dw_next = sum_t dxn ohat,  dgate[j] = sum over its tokens of dR w yhat
+ * dR is held in fp32. dr [T][d] of out's type (may be dout), dy [T][d] bf16,
+ * dw and dw_next [d], dgate [ceil(T / gate_rows)][d] fp32. Without a next norm
+ * w_next, dxn, out, rstd_next and dw_next are not used (w_next, dxn and dw_next must be NULL). */
+moe_status_t moe_block_norm_out_backward(const void* dout, const moe_bf16_t* dxn, const moe_bf16_t* y, const void* out,
+                                         moe_stream_type_t type, const float* w, const moe_bf16_t* gate, int gate_rows,
+                                         float alpha, const float* w_next, const float* rstd, const float* rstd_next,
+                                         int T, int d, void* dr, moe_bf16_t* dy, float* dw, float* dgate,
+                                         float* dw_next, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ---- Measurement and test hook ----
  * The bf16 grouped GEMMs (moe_grouped_gemm_gateup / _down) pick one of
  * several kernel families from the problem's shape. All of them compute the

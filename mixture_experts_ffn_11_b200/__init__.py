@@ -5,10 +5,12 @@ Python binding (``_native``) plus a layer object that owns buffers and calls the
 (``layer.MoEFFN``). Importing the package loads the library and fails if it has not been built.
 """
 from . import _native
-from ._native import (MoEError, ROUTE_MODES, get_device_error, grouped_gemm_down, grouped_gemm_gateup, permute,
-                      permute_workspace_size, route_topk, topk_from_logits, unpermute_combine)
+from ._native import (MoEError, ROUTE_MODES, block_norm_backward_workspace_size, block_norm_in, block_norm_in_backward,
+                      block_norm_out, block_norm_out_backward, get_device_error, grouped_gemm_down, grouped_gemm_gateup,
+                      permute, permute_workspace_size, route_topk, topk_from_logits, unpermute_combine)
 from .layer import MoEFFN
 
 __all__ = ["MoEFFN", "MoEError", "ROUTE_MODES", "route_topk", "topk_from_logits", "permute",
            "permute_workspace_size", "grouped_gemm_gateup", "grouped_gemm_down", "unpermute_combine",
-           "get_device_error"]
+           "block_norm_in", "block_norm_out", "block_norm_in_backward", "block_norm_out_backward",
+           "block_norm_backward_workspace_size", "get_device_error"]

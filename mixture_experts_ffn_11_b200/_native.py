@@ -31,7 +31,8 @@ EXPORTS = ("moe_route_topk", "moe_router_split_weights", "moe_route_topk_split",
            "moe_grouped_gemm_gateup_save",
            "moe_swiglu_backward", "moe_permute_backward", "moe_transpose_weights",
            "moe_grouped_weight_grad_workspace_size", "moe_grouped_weight_grad", "moe_router_backward_workspace_size",
-           "moe_router_backward", "moe_set_gemm_kernel", "moe_test_set_wait", "moe_get_device_error",
+           "moe_router_backward", "moe_block_norm_in", "moe_block_norm_out", "moe_block_norm_backward_workspace_size",
+           "moe_block_norm_in_backward", "moe_block_norm_out_backward", "moe_set_gemm_kernel", "moe_test_set_wait", "moe_get_device_error",
            "moe_last_error_string")
 GEMM_KERNELS = {"auto": 0, "single": 1, "pair": 2, "wide": 3, "swap": 4}
 
@@ -47,7 +48,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise ImportError(f"{path} is not built; run `python mixture_experts_ffn_11_b200/build.py` "
                           "(there is no non-CUDA fallback)")
     lib = ctypes.CDLL(path)
-    vp, ci, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, ci, sz, cf = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     sig = {
         "moe_route_topk": [vp, vp, vp, ci, ci, ci, ci, ci, vp, vp, vp, vp],
         "moe_router_split_weights": [vp, ci, ci, vp, vp],
@@ -76,6 +77,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_weight_grad": [vp, vp, vp, ci, ci, ci, ci, vp, vp, sz, vp],
         "moe_router_backward_workspace_size": [ci, ci, ci, ci],
         "moe_router_backward": [vp, vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp, vp, vp, vp, vp, sz, vp],
+        "moe_block_norm_in": [vp, ci, vp, ci, ci, cf, vp, vp, vp],
+        "moe_block_norm_out": [vp, vp, ci, vp, vp, ci, cf, vp, ci, ci, cf, vp, vp, vp, vp, vp],
+        "moe_block_norm_backward_workspace_size": [ci, ci, ci],
+        "moe_block_norm_in_backward": [vp, vp, vp, ci, vp, vp, ci, ci, vp, vp, vp, sz, vp],
+        "moe_block_norm_out_backward": [vp, vp, vp, vp, ci, vp, vp, ci, cf, vp, vp, vp, ci, ci, vp, vp, vp, vp, vp, vp,
+                                        sz, vp],
         "moe_set_gemm_kernel": [ci],
         "moe_test_set_wait": [ctypes.c_ulonglong, ci],
         "moe_get_device_error": [ctypes.POINTER(ctypes.c_uint), vp],
@@ -90,6 +97,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_grouped_gemm_gateup_gather_workspace_size.restype = sz
     lib.moe_grouped_gemm_down_combine_workspace_size.restype = sz
     lib.moe_router_backward_workspace_size.restype = sz
+    lib.moe_block_norm_backward_workspace_size.restype = sz
     lib.moe_last_error_string.restype = ctypes.c_char_p
     return lib
 
@@ -451,6 +459,135 @@ def router_backward(x, w_router, logits, topk_idx, topk_w, dw, perm_src, inv_per
                                     _p(inv_perm), _p(expert_offsets), T, d, E, k, ROUTE_MODES[mode], _p(dx_addend),
                                     _p(dx), _p(dw_router), _p(dbias), _p(ws), ws_bytes, _stream(stream)),
            "moe_router_backward")
+
+
+# ---- norms around a block ----
+
+STREAM_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # moe_stream_type_t
+
+
+def _want(t, dtype, shape, name, dev):
+    """data_ptr of a contiguous CUDA tensor of this type and shape on device index `dev`; ValueError otherwise."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'} on {t.device}")
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    """Index of the CUDA device that holds t; the call runs there, whichever device is current."""
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name}: want a CUDA tensor, got {t if t is None else t.device}")
+    return t.get_device()
+
+
+def _run(what, fn, dev, stream, *args):
+    """Call a library entry point on device `dev`, on `stream` (default: that device's current stream)."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"{what}: a stream of cuda:{dev} is needed, got one of {stream.device}")
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != MOE_OK:
+        _check(status, what)
+
+
+def _ws(t, dev):
+    """(data_ptr, bytes) of a uint8 workspace, (None, 0) for None."""
+    if t is None:
+        return None, 0
+    return _want(t, torch.uint8, t.shape, "ws", dev), t.numel()
+
+
+def _stream_type(t, name):
+    if t.dtype not in STREAM_TYPES:
+        raise ValueError(f"{name}: want torch.bfloat16 or torch.float32, got {t.dtype}")
+    return STREAM_TYPES[t.dtype]
+
+
+def _gate_ptr(gate, gate_rows, T, d, dev, dtype=torch.bfloat16, name="gate"):
+    if gate is None and gate_rows == 0:
+        return None
+    if gate_rows < 1:
+        raise ValueError(f"gate_rows={gate_rows}: at least 1 with a gate, 0 without")
+    return _want(gate, dtype, (-(-T // gate_rows), d), name, dev)
+
+
+def block_norm_in(x, w, eps, xn, rstd, stream=None):
+    """xn [T, d] bf16 <- x * rstd * w, rstd [T] fp32 <- (mean x^2 + eps)^(-1/2); x [T, d] bf16 or fp32, w [d] fp32."""
+    dev = _device_of(x, "x")
+    T, d = x.shape
+    _run("moe_block_norm_in", _lib.moe_block_norm_in, dev, stream, _want(x, x.dtype, (T, d), "x", dev), _stream_type(x, "x"),
+         _want(w, torch.float32, (d,), "w", dev), T, d, eps, _want(xn, torch.bfloat16, (T, d), "xn", dev),
+         _want(rstd, torch.float32, (T,), "rstd", dev))
+
+
+def block_norm_out(y, r, w, gate, gate_rows, alpha, w_next, eps, out, rstd, xn=None, rstd_next=None, stream=None):
+    """out [T, d] <- alpha * r + gate * (y * rstd * w); with w_next, xn [T, d] bf16 <- out * rstd_next * w_next in the same
+    pass. y [T, d] bf16; r and out bf16 or fp32 (out may be r); gate [ceil(T / gate_rows), d] bf16, or None with
+    gate_rows = 0; w, w_next [d], rstd, rstd_next [T] fp32."""
+    dev = _device_of(y, "y")
+    T, d = y.shape
+    f32, bf = torch.float32, torch.bfloat16
+    kind = _stream_type(r, "r")
+    nxt = (None, None, None)
+    if w_next is not None:
+        nxt = (_want(w_next, f32, (d,), "w_next", dev), _want(xn, bf, (T, d), "xn", dev),
+               _want(rstd_next, f32, (T,), "rstd_next", dev))
+    _run("moe_block_norm_out", _lib.moe_block_norm_out, dev, stream, _want(y, bf, (T, d), "y", dev),
+         _want(r, r.dtype, (T, d), "r", dev), kind, _want(w, f32, (d,), "w", dev), _gate_ptr(gate, gate_rows, T, d, dev),
+         gate_rows, alpha, nxt[0], T, d, eps, _want(out, r.dtype, (T, d), "out", dev), _want(rstd, f32, (T,), "rstd", dev),
+         nxt[1], nxt[2])
+
+
+def block_norm_backward_workspace_size(T: int, d: int, gate_rows: int = 0) -> int:
+    return int(_lib.moe_block_norm_backward_workspace_size(T, d, gate_rows))
+
+
+def block_norm_in_backward(dxn, dres, x, w, rstd, dx, dw, ws, stream=None):
+    """dx [T, d] <- dres + the gradient of block_norm_in for dxn [T, d] bf16; dw [d] fp32. dres [T, d] of x's type, or None;
+    dx may be dres. ws: block_norm_backward_workspace_size(T, d) bytes."""
+    dev = _device_of(x, "x")
+    T, d = x.shape
+    f32 = torch.float32
+    _run("moe_block_norm_in_backward", _lib.moe_block_norm_in_backward, dev, stream,
+         _want(dxn, torch.bfloat16, (T, d), "dxn", dev), None if dres is None else _want(dres, x.dtype, (T, d), "dres", dev),
+         _want(x, x.dtype, (T, d), "x", dev), _stream_type(x, "x"), _want(w, f32, (d,), "w", dev),
+         _want(rstd, f32, (T,), "rstd", dev), T, d, _want(dx, x.dtype, (T, d), "dx", dev), _want(dw, f32, (d,), "dw", dev),
+         *_ws(ws, dev))
+
+
+def block_norm_out_backward(dout, dxn, y, out, w, gate, gate_rows, alpha, w_next, rstd, rstd_next, dr, dy, dw, dgate, dw_next,
+                            ws, stream=None):
+    """Gradients of block_norm_out: dr [T, d] (type of dout; may be dout), dy [T, d] bf16, dw and dw_next [d] fp32, dgate
+    [ceil(T / gate_rows), d] fp32, from dout [T, d] along the residual stream and, with w_next, dxn [T, d] bf16 through the
+    next norm (out: the forward's output). ws: block_norm_backward_workspace_size(T, d, gate_rows) bytes."""
+    dev = _device_of(y, "y")
+    T, d = y.shape
+    f32, bf = torch.float32, torch.bfloat16
+    kind = _stream_type(dout, "dout")
+    if w_next is None:
+        if dxn is not None or dw_next is not None:
+            raise ValueError("dxn and dw_next belong to a next norm: w_next is None")
+        nxt = (None, None, None, None, None)
+    else:
+        nxt = (_want(dxn, bf, (T, d), "dxn", dev), _want(out, dout.dtype, (T, d), "out", dev),
+               _want(w_next, f32, (d,), "w_next", dev), _want(rstd_next, f32, (T,), "rstd_next", dev),
+               _want(dw_next, f32, (d,), "dw_next", dev))
+    _run("moe_block_norm_out_backward", _lib.moe_block_norm_out_backward, dev, stream,
+         _want(dout, dout.dtype, (T, d), "dout", dev), nxt[0], _want(y, bf, (T, d), "y", dev), nxt[1], kind,
+         _want(w, f32, (d,), "w", dev), _gate_ptr(gate, gate_rows, T, d, dev), gate_rows, alpha, nxt[2],
+         _want(rstd, f32, (T,), "rstd", dev), nxt[3], T, d, _want(dr, dout.dtype, (T, d), "dr", dev),
+         _want(dy, bf, (T, d), "dy", dev), _want(dw, f32, (d,), "dw", dev),
+         _gate_ptr(dgate, gate_rows, T, d, dev, f32, "dgate"), nxt[4], *_ws(ws, dev))
 
 
 def set_gemm_kernel(name: str) -> None:

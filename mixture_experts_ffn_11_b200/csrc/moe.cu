@@ -25,6 +25,7 @@
 #include "gemm_wgrad.cuh"
 #include "backward.cuh"
 #include "combine.cuh"
+#include "block_norm.cuh"
 
 using namespace moe;
 
@@ -782,6 +783,114 @@ moe_status_t route_impl(const moe_bf16_t* x, const float* w_router, const moe_bf
 
 }  // namespace
 
+// ---- block norms ----
+namespace {
+
+// Threads and vectors per thread for rows of d columns. Few rows (a decoding step): one vector per thread where that fits,
+// for the shortest path through a row.
+struct NormShape {
+    int vpt, threads;
+};
+NormShape norm_shape(int T, int d, int sms) {
+    const int nvec = d / 8;
+    int vpt = nvec <= 128 ? 1 : (nvec <= 2 * BN_MAX_THREADS ? 2 : 4);
+    if (T <= sms && nvec <= BN_MAX_THREADS) vpt = 1;
+    return {vpt, (nvec + vpt * 32 - 1) / (vpt * 32) * 32};
+}
+
+moe_status_t check_norm_sizes(int T, int d, moe_stream_type_t type) {
+    if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T=%d < 0", T);
+    if (d < 8 || d % 8 || d > BN_MAX_D)
+        return fail(MOE_ERR_INVALID_ARG, "d=%d must be a positive multiple of 8, at most %d", d, BN_MAX_D);
+    if (type != MOE_STREAM_BF16 && type != MOE_STREAM_FP32)
+        return fail(MOE_ERR_INVALID_ARG, "unknown residual type %d", (int)type);
+    return MOE_OK;
+}
+
+moe_status_t check_norm_eps(float eps) {
+    if (!(eps >= 0.f) || eps > 1e30f) return fail(MOE_ERR_INVALID_ARG, "eps=%g must be finite and not negative", (double)eps);
+    return MOE_OK;
+}
+
+// (without tokens the gate has no rows, and its pointer may be null)
+moe_status_t check_norm_gate(const void* gate, int gate_rows, int T) {
+    if (gate_rows < 0 || (T > 0 && (gate != nullptr) != (gate_rows > 0)))
+        return fail(MOE_ERR_INVALID_ARG, "gate_rows=%d: at least 1 with a gate, 0 without", gate_rows);
+    return MOE_OK;
+}
+
+int norm_grad_ctas(int T) { return T < BN_GRAD_CTAS ? T : BN_GRAD_CTAS; }
+
+#define MOE_NORM_VPT(vpt, CALL)        \
+    switch (vpt) {                     \
+        case 1: CALL(1); break;        \
+        case 2: CALL(2); break;        \
+        default: CALL(4); break;       \
+    }
+
+template <typename R>
+cudaError_t launch_norm_in(const void* x, const float* w, int T, int d, float eps, void* xn, float* rstd, int sms,
+                           cudaStream_t stream) {
+    const NormShape s = norm_shape(T, d, sms);
+    const int grid = grid_cap(T, sms, std::max(1, 1536 / s.threads));
+    cudaError_t e = cudaSuccess;
+#define CALL(V)                                                                                                   \
+    e = launch_pdl(block_norm_in_kernel<R, V>, dim3(grid), dim3(s.threads), 0, stream, reinterpret_cast<const R*>(x), w, T, d, \
+                   eps, reinterpret_cast<__nv_bfloat16*>(xn), rstd)
+    MOE_NORM_VPT(s.vpt, CALL)
+#undef CALL
+    return e;
+}
+
+template <typename R, bool NEXT>
+cudaError_t launch_norm_out(const NormOutArgs& a, int sms, cudaStream_t stream) {
+    const NormShape s = norm_shape(a.T, a.d, sms);
+    const int grid = grid_cap(a.T, sms, std::max(1, 1024 / s.threads));
+    cudaError_t e = cudaSuccess;
+#define CALL(V) e = launch_pdl(block_norm_out_kernel<R, V, NEXT>, dim3(grid), dim3(s.threads), 0, stream, a)
+    MOE_NORM_VPT(s.vpt, CALL)
+#undef CALL
+    return e;
+}
+
+template <typename R>
+cudaError_t launch_norm_in_grad(const NormInGradArgs& a, int sms, cudaStream_t stream) {
+    const NormShape s = norm_shape(a.T, a.d, sms);
+    cudaError_t e = cudaSuccess;
+#define CALL(V) e = launch_plain(block_norm_in_grad_kernel<R, V>, dim3(norm_grad_ctas(a.T)), dim3(s.threads), 0, stream, a)
+    MOE_NORM_VPT(s.vpt, CALL)
+#undef CALL
+    return e;
+}
+
+template <typename R, bool NEXT, bool GATE>
+cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int sms, cudaStream_t stream) {
+    const NormShape s = norm_shape(a.T, a.d, sms);
+    cudaError_t e = cudaSuccess;
+#define CALL(V) \
+    e = launch_plain(block_norm_out_grad_kernel<R, V, NEXT, GATE>, dim3(norm_grad_ctas(a.T)), dim3(s.threads), 0, stream, a)
+    MOE_NORM_VPT(s.vpt, CALL)
+#undef CALL
+    return e;
+}
+
+template <typename R>
+cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int sms, cudaStream_t stream) {
+    if (a.dxn)
+        return a.gate ? launch_norm_out_grad<R, true, true>(a, sms, stream) : launch_norm_out_grad<R, true, false>(a, sms, stream);
+    return a.gate ? launch_norm_out_grad<R, false, true>(a, sms, stream) : launch_norm_out_grad<R, false, false>(a, sms, stream);
+}
+
+cudaError_t launch_norm_reduce(const NormReduceArgs& a, cudaStream_t stream) {
+    return launch_plain(block_norm_reduce_kernel, dim3((a.d + 31) / 32, a.part_gate ? a.B + 1 : 2), dim3(BNR_WARPS * 32), 0, stream,
+                        a);
+}
+
+// Workspace of a backward pass: part_w [B][d] | part_next [B][d] | part_gate [B][2][d] (with a gate)
+size_t norm_grad_ws(int T, int d, int gate_rows) { return (size_t)norm_grad_ctas(T) * d * 4 * (gate_rows > 0 ? 4 : 2); }
+
+}  // namespace
+
 extern "C" {
 
 moe_status_t moe_route_topk(const moe_bf16_t* x, const float* w_router, const float* bias, int T, int d, int E,
@@ -1319,6 +1428,127 @@ moe_status_t moe_router_backward(const moe_bf16_t* x, const float* w_router, con
                    (const float*)dl_tk, w_router, reinterpret_cast<const __nv_bfloat16*>(dx_addend), T, d, E, k,
                    reinterpret_cast<__nv_bfloat16*>(dx));
     return check_launch("router_input_grad", e);
+}
+
+// ---- block norms ----
+
+moe_status_t moe_block_norm_in(const void* x, moe_stream_type_t type, const float* w, int T, int d, float eps,
+                               moe_bf16_t* xn, float* rstd, cudaStream_t stream) {
+    moe_status_t st = check_norm_sizes(T, d, type);
+    if (st == MOE_OK) st = check_norm_eps(eps);
+    if (st != MOE_OK) return st;
+    if (!w || (T > 0 && (!x || !xn || !rstd))) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(x) || !aligned16(w) || !aligned16(xn)) return fail(MOE_ERR_INVALID_ARG, "x, w and xn must be 16-byte aligned");
+    DeviceInfo di;
+    if ((st = device_info(di)) != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    return check_launch("block_norm_in", type == MOE_STREAM_FP32 ? launch_norm_in<float>(x, w, T, d, eps, xn, rstd, di.sms, stream)
+                                                                 : launch_norm_in<__nv_bfloat16>(x, w, T, d, eps, xn, rstd, di.sms,
+                                                                                                 stream));
+}
+
+moe_status_t moe_block_norm_out(const moe_bf16_t* y, const void* r, moe_stream_type_t type, const float* w,
+                                const moe_bf16_t* gate, int gate_rows, float alpha, const float* w_next, int T, int d,
+                                float eps, void* out, float* rstd, moe_bf16_t* xn, float* rstd_next, cudaStream_t stream) {
+    moe_status_t st = check_norm_sizes(T, d, type);
+    if (st == MOE_OK) st = check_norm_eps(eps);
+    if (st == MOE_OK) st = check_norm_gate(gate, gate_rows, T);
+    if (st != MOE_OK) return st;
+    if (!w || (T > 0 && (!y || !r || !out || !rstd || (w_next && (!xn || !rstd_next)))))
+        return fail(MOE_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(y) || !aligned16(r) || !aligned16(w) || !aligned16(gate) || !aligned16(w_next) || !aligned16(out) ||
+        !aligned16(xn))
+        return fail(MOE_ERR_INVALID_ARG, "y, r, w, gate, w_next, out and xn must be 16-byte aligned");
+    DeviceInfo di;
+    if ((st = device_info(di)) != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    const NormOutArgs a{reinterpret_cast<const __nv_bfloat16*>(y), r, w, reinterpret_cast<const __nv_bfloat16*>(gate), w_next, out,
+                        rstd, reinterpret_cast<__nv_bfloat16*>(xn), rstd_next, T, d, gate_rows, alpha, eps};
+    const bool f32 = type == MOE_STREAM_FP32;
+    cudaError_t e;
+    if (w_next)
+        e = f32 ? launch_norm_out<float, true>(a, di.sms, stream) : launch_norm_out<__nv_bfloat16, true>(a, di.sms, stream);
+    else
+        e = f32 ? launch_norm_out<float, false>(a, di.sms, stream) : launch_norm_out<__nv_bfloat16, false>(a, di.sms, stream);
+    return check_launch("block_norm_out", e);
+}
+
+size_t moe_block_norm_backward_workspace_size(int T, int d, int gate_rows) {
+    if (T <= 0 || d <= 0) return 0;
+    return round256(norm_grad_ws(T, d, gate_rows));
+}
+
+moe_status_t moe_block_norm_in_backward(const moe_bf16_t* dxn, const void* dres, const void* x, moe_stream_type_t type,
+                                        const float* w, const float* rstd, int T, int d, void* dx, float* dw, void* ws,
+                                        size_t ws_bytes, cudaStream_t stream) {
+    moe_status_t st = check_norm_sizes(T, d, type);
+    if (st != MOE_OK) return st;
+    if (!w || !dw || (T > 0 && (!dxn || !x || !rstd || !dx))) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(dxn) || !aligned16(dres) || !aligned16(x) || !aligned16(w) || !aligned16(dx))
+        return fail(MOE_ERR_INVALID_ARG, "dxn, dres, x, w and dx must be 16-byte aligned");
+    const size_t need = T > 0 ? norm_grad_ws(T, d, 0) : 0;
+    if (need && (!ws || ws_bytes < need))
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
+    if (need && !aligned16(ws)) return fail(MOE_ERR_WORKSPACE, "workspace not 16-byte aligned");
+    DeviceInfo di;
+    if ((st = device_info(di)) != MOE_OK) return st;
+    if (T == 0) {  // no tokens: the gain's gradient is zero
+        const cudaError_t e = cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)d, stream);
+        return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
+    }
+    const NormInGradArgs a{reinterpret_cast<const __nv_bfloat16*>(dxn), dres, x, w, rstd, dx, reinterpret_cast<float*>(ws), T, d};
+    cudaError_t e = type == MOE_STREAM_FP32 ? launch_norm_in_grad<float>(a, di.sms, stream)
+                                            : launch_norm_in_grad<__nv_bfloat16>(a, di.sms, stream);
+    if ((st = check_launch("block_norm_in_backward", e)) != MOE_OK) return st;
+    NormReduceArgs ra{};
+    ra.part_w = a.part_w;
+    ra.dw = dw;
+    ra.T = T, ra.d = d, ra.B = norm_grad_ctas(T);
+    return check_launch("block_norm_in_backward (sums)", launch_norm_reduce(ra, stream));
+}
+
+moe_status_t moe_block_norm_out_backward(const void* dout, const moe_bf16_t* dxn, const moe_bf16_t* y, const void* out,
+                                         moe_stream_type_t type, const float* w, const moe_bf16_t* gate, int gate_rows,
+                                         float alpha, const float* w_next, const float* rstd, const float* rstd_next, int T,
+                                         int d, void* dr, moe_bf16_t* dy, float* dw, float* dgate, float* dw_next, void* ws,
+                                         size_t ws_bytes, cudaStream_t stream) {
+    moe_status_t st = check_norm_sizes(T, d, type);
+    if (st == MOE_OK) st = check_norm_gate(gate, gate_rows, T);
+    if (st != MOE_OK) return st;
+    if (!w || !dw || (T > 0 && (!dout || !y || !rstd || !dr || !dy))) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+    if ((w_next != nullptr) != (dw_next != nullptr) || (!w_next && dxn) || (T > 0 && w_next && (!dxn || !out || !rstd_next)))
+        return fail(MOE_ERR_INVALID_ARG, "the next norm takes w_next, dxn, out, rstd_next and dw_next together");
+    if (T > 0 && gate && !dgate) return fail(MOE_ERR_INVALID_ARG, "a gate needs dgate");
+    if (!aligned16(dout) || !aligned16(dxn) || !aligned16(y) || !aligned16(out) || !aligned16(w) || !aligned16(gate) ||
+        !aligned16(w_next) || !aligned16(dr) || !aligned16(dy) || !aligned16(dgate))
+        return fail(MOE_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    const size_t need = T > 0 ? norm_grad_ws(T, d, gate_rows) : 0;
+    if (need && (!ws || ws_bytes < need))
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
+    if (need && !aligned16(ws)) return fail(MOE_ERR_WORKSPACE, "workspace not 16-byte aligned");
+    DeviceInfo di;
+    if ((st = device_info(di)) != MOE_OK) return st;
+    if (T == 0) {  // no tokens: the gains' gradients are zero
+        cudaError_t e = cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)d, stream);
+        if (e == cudaSuccess && dw_next) e = cudaMemsetAsync(dw_next, 0, sizeof(float) * (size_t)d, stream);
+        return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
+    }
+    const int B = norm_grad_ctas(T);
+    float* part = reinterpret_cast<float*>(ws);
+    NormOutGradArgs a{};
+    a.dout = dout, a.dxn = reinterpret_cast<const __nv_bfloat16*>(dxn), a.y = reinterpret_cast<const __nv_bfloat16*>(y);
+    a.out = out, a.w = w, a.gate = reinterpret_cast<const __nv_bfloat16*>(gate), a.w_next = w_next;
+    a.rstd = rstd, a.rstd_next = rstd_next, a.dr = dr, a.dy = reinterpret_cast<__nv_bfloat16*>(dy), a.dgate = dgate;
+    a.part_w = part, a.part_next = part + (size_t)B * d, a.part_gate = part + (size_t)2 * B * d;
+    a.T = T, a.d = d, a.gate_rows = gate_rows, a.alpha = alpha;
+    cudaError_t e = type == MOE_STREAM_FP32 ? launch_norm_out_grad<float>(a, di.sms, stream)
+                                            : launch_norm_out_grad<__nv_bfloat16>(a, di.sms, stream);
+    if ((st = check_launch("block_norm_out_backward", e)) != MOE_OK) return st;
+    NormReduceArgs ra{};
+    ra.part_w = a.part_w, ra.part_next = dxn ? a.part_next : nullptr, ra.part_gate = gate ? a.part_gate : nullptr;
+    ra.dw = dw, ra.dw_next = dw_next, ra.dgate = dgate;
+    ra.T = T, ra.d = d, ra.gate_rows = gate_rows, ra.B = B;
+    return check_launch("block_norm_out_backward (sums)", launch_norm_reduce(ra, stream));
 }
 
 moe_status_t moe_set_gemm_kernel(moe_gemm_kernel_t kind) {
