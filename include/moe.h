@@ -332,6 +332,53 @@ moe_status_t moe_grouped_gemm_down_mxfp4(const moe_bf16_t* h, const uint8_t* wq_
                                          const int32_t* group_offsets, int G, int M, int d, int f, moe_bf16_t* y,
                                          cudaStream_t stream);
 
+/* ---- e4m3 expert products with a scale per block of 128 ----
+ * Expert weights and activations in FP8 E4M3 (sign, 4 exponent bits with bias
+ * 7, 3 mantissa bits, largest magnitude 448, no infinities), half the bytes of
+ * bf16 and twice its tensor-core rate. Each block of 128 values along the
+ * reduction axis K shares one fp32 scale: activations per row and 128
+ * columns, weights per 128 x 128 block; the last block of a row, column or
+ * matrix may be partial. A value stands for q * scale. With top the largest
+ * magnitude of a block:
+ *   scale = top / 448 (1 for a block of zeros), q = 448 x / top rounded to the
+ *   nearest e4m3, ties to even (the quotient is not rounded before)
+ * Layouts (nb(n) = ceil(n / 128)):
+ *   activations  q [R][K] uint8 (e4m3 bits), s [nb(K)][R] fp32
+ *   weights      q [G][N][K], s [G][nb(N)][nb(K)]; a gate|up tensor [G][2f][d]
+ *                is blocked apart for gate and up: it is quantized as 2G
+ *                matrices [f][d], s [G][2][nb(f)][nb(d)]
+ * A block that holds an infinity or NaN gives NaN, in the rows it belongs to.
+ * Weights and scales of another origin (a checkpoint's) may be passed as they
+ * are: any finite fp32 scales. */
+
+/* Encode w [G][N][K] (layout above). K a positive multiple of 16; w, q 16-byte
+ * aligned; G = 0 or N = 0 is an empty no-op. */
+moe_status_t moe_fp8_block_quantize(const moe_bf16_t* w, int G, int N, int K, uint8_t* q, float* s,
+                                    cudaStream_t stream);
+
+/* Encode R rows: row r is x[row_src[r]] of x [T][K] (the dispatch of section
+ * "Expert Backend" folded into the encoding), or x[r] with row_src NULL
+ * (R <= T). q [R][K], s [nb(K)][R]. An entry of row_src outside [0, T) is
+ * flagged (MOE_DEVERR_ROW_RANGE) and its row encoded as zeros. */
+moe_status_t moe_fp8_row_quantize(const moe_bf16_t* x, const int32_t* row_src, int T, int K, int R, uint8_t* q,
+                                  float* s, cudaStream_t stream);
+
+/* moe_grouped_gemm_gateup on e4m3 operands: aq [M][d], as [nb(d)][M], wq_gateup
+ * [G][2f][d], ws_gateup [G][2][nb(f)][nb(d)], h [M][f] bf16. Products of a
+ * block of 128 are summed by the tensor cores in fp32, the blocks' sums times
+ * their scales in fp32 registers; h is rounded once. d, f positive multiples of
+ * 16; rows at or past group_offsets[G] are not written; other limits as
+ * moe_grouped_gemm_gateup. */
+moe_status_t moe_grouped_gemm_gateup_fp8(const uint8_t* aq, const float* as, const uint8_t* wq_gateup,
+                                         const float* ws_gateup, const int32_t* group_offsets, int G, int M, int d,
+                                         int f, moe_bf16_t* h, cudaStream_t stream);
+
+/* moe_grouped_gemm_down on e4m3 operands: hq [M][f], hs [nb(f)][M], wq_down
+ * [G][d][f], ws_down [G][nb(d)][nb(f)], y [M][d] bf16. Limits as above. */
+moe_status_t moe_grouped_gemm_down_fp8(const uint8_t* hq, const float* hs, const uint8_t* wq_down,
+                                       const float* ws_down, const int32_t* group_offsets, int G, int M, int d, int f,
+                                       moe_bf16_t* y, cudaStream_t stream);
+
 /* Apply the routing weights and return to token order ("apply the routing
  * weights and then collect and reorder the results", section "Expert
  * Backend"): y[t][c] = sum_{j<k} topk_w[t][j] * y_perm[inv_perm[t*k+j]][c]

@@ -27,7 +27,8 @@ EXPORTS = ("moe_route_topk", "moe_router_split_weights", "moe_route_topk_split",
            "moe_grouped_gemm_gateup", "moe_grouped_gemm_gateup_gather_workspace_size",
            "moe_grouped_gemm_gateup_gather", "moe_gather_rows", "moe_grouped_gemm_down",
            "moe_grouped_gemm_down_combine_workspace_size", "moe_grouped_gemm_down_combine", "moe_mxfp4_quantize", "moe_grouped_gemm_gateup_mxfp4",
-           "moe_grouped_gemm_down_mxfp4", "moe_unpermute_combine", "moe_grouped_gemm_gateup_preact",
+           "moe_grouped_gemm_down_mxfp4", "moe_fp8_block_quantize", "moe_fp8_row_quantize",
+           "moe_grouped_gemm_gateup_fp8", "moe_grouped_gemm_down_fp8", "moe_unpermute_combine", "moe_grouped_gemm_gateup_preact",
            "moe_grouped_gemm_gateup_save",
            "moe_swiglu_backward", "moe_permute_backward", "moe_transpose_weights",
            "moe_grouped_weight_grad_workspace_size", "moe_grouped_weight_grad", "moe_router_backward_workspace_size",
@@ -67,6 +68,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_mxfp4_quantize": [vp, ci, ci, ci, vp, vp, vp],
         "moe_grouped_gemm_gateup_mxfp4": [vp, vp, vp, vp, ci, ci, ci, ci, vp, vp],
         "moe_grouped_gemm_down_mxfp4": [vp, vp, vp, vp, ci, ci, ci, ci, vp, vp],
+        "moe_fp8_block_quantize": [vp, ci, ci, ci, vp, vp, vp],
+        "moe_fp8_row_quantize": [vp, vp, ci, ci, ci, vp, vp, vp],
+        "moe_grouped_gemm_gateup_fp8": [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp, vp],
+        "moe_grouped_gemm_down_fp8": [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp, vp],
         "moe_unpermute_combine": [vp, vp, vp, vp, ci, ci, ci, vp, vp],
         "moe_grouped_gemm_gateup_preact": [vp, vp, vp, ci, ci, ci, ci, vp, vp],
         "moe_grouped_gemm_gateup_save": [vp, vp, vp, ci, ci, ci, ci, vp, vp, vp],
@@ -461,10 +466,7 @@ def router_backward(x, w_router, logits, topk_idx, topk_w, dw, perm_src, inv_per
            "moe_router_backward")
 
 
-# ---- norms around a block ----
-
-STREAM_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # moe_stream_type_t
-
+# ---- calls on the device that holds the tensors ----
 
 def _want(t, dtype, shape, name, dev):
     """data_ptr of a contiguous CUDA tensor of this type and shape on device index `dev`; ValueError otherwise."""
@@ -505,6 +507,68 @@ def _ws(t, dev):
     if t is None:
         return None, 0
     return _want(t, torch.uint8, t.shape, "ws", dev), t.numel()
+
+
+# ---- e4m3 values with a scale per block of 128 ----
+
+E4M3 = torch.float8_e4m3fn
+
+
+def fp8_blocks(n: int) -> int:
+    """Blocks of 128 that n values take."""
+    return (n + 127) // 128
+
+
+def fp8_block_quantize(w, q, s, stream=None):
+    """Encode bf16 weights w [G, N, K] as e4m3 q [G, N, K] with a scale per 128 x 128 block, s [G, ceil(N/128), ceil(K/128)]
+    fp32. A gate|up tensor [G, 2f, d] is encoded as 2G matrices: w.view(2 G, f, d)."""
+    dev = _device_of(w, "w")
+    G, n, K = w.shape
+    _run("moe_fp8_block_quantize", _lib.moe_fp8_block_quantize, dev, stream, _want(w, torch.bfloat16, (G, n, K), "w", dev), G, n,
+         K, _want(q, E4M3, (G, n, K), "q", dev), _want(s, torch.float32, (G, fp8_blocks(n), fp8_blocks(K)), "s", dev))
+
+
+def fp8_row_quantize(x, row_src, q, s, stream=None):
+    """Encode rows x[row_src[r]] (x[r] with row_src None) of x [T, K] bf16 as e4m3 q [R, K] with a scale per row and 128
+    columns, s [ceil(K/128), R] fp32."""
+    dev = _device_of(x, "x")
+    T, K = x.shape
+    R = q.shape[0]
+    _run("moe_fp8_row_quantize", _lib.moe_fp8_row_quantize, dev, stream, _want(x, torch.bfloat16, (T, K), "x", dev),
+         None if row_src is None else _want(row_src, torch.int32, (R,), "row_src", dev), T, K, R, _want(q, E4M3, (R, K), "q", dev),
+         _want(s, torch.float32, (fp8_blocks(K), R), "s", dev))
+
+
+def grouped_gemm_gateup_fp8(aq, a_s, wq_gateup, ws_gateup, group_offsets, h, stream=None):
+    """h [M, f] bf16 <- silu(gate) * up of e4m3 rows aq [M, d] (scales a_s [ceil(d/128), M]) and weights wq_gateup [G, 2f, d]
+    (scales ws_gateup [G, 2, ceil(f/128), ceil(d/128)])."""
+    dev = _device_of(aq, "aq")
+    M, d = aq.shape
+    G, two_f, _ = wq_gateup.shape
+    f = two_f // 2
+    f32 = torch.float32
+    _run("moe_grouped_gemm_gateup_fp8", _lib.moe_grouped_gemm_gateup_fp8, dev, stream, _want(aq, E4M3, (M, d), "aq", dev),
+         _want(a_s, f32, (fp8_blocks(d), M), "a_s", dev), _want(wq_gateup, E4M3, (G, 2 * f, d), "wq_gateup", dev),
+         _want(ws_gateup, f32, (G, 2, fp8_blocks(f), fp8_blocks(d)), "ws_gateup", dev),
+         _want(group_offsets, torch.int32, (G + 1,), "group_offsets", dev), G, M, d, f, _want(h, torch.bfloat16, (M, f), "h", dev))
+
+
+def grouped_gemm_down_fp8(hq, h_s, wq_down, ws_down, group_offsets, y, stream=None):
+    """y [M, d] bf16 <- the down product of e4m3 rows hq [M, f] (scales h_s [ceil(f/128), M]) and weights wq_down [G, d, f]
+    (scales ws_down [G, ceil(d/128), ceil(f/128)])."""
+    dev = _device_of(hq, "hq")
+    M, f = hq.shape
+    G, d, _ = wq_down.shape
+    f32 = torch.float32
+    _run("moe_grouped_gemm_down_fp8", _lib.moe_grouped_gemm_down_fp8, dev, stream, _want(hq, E4M3, (M, f), "hq", dev),
+         _want(h_s, f32, (fp8_blocks(f), M), "h_s", dev), _want(wq_down, E4M3, (G, d, f), "wq_down", dev),
+         _want(ws_down, f32, (G, fp8_blocks(d), fp8_blocks(f)), "ws_down", dev),
+         _want(group_offsets, torch.int32, (G + 1,), "group_offsets", dev), G, M, d, f, _want(y, torch.bfloat16, (M, d), "y", dev))
+
+
+# ---- norms around a block ----
+
+STREAM_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # moe_stream_type_t
 
 
 def _stream_type(t, name):

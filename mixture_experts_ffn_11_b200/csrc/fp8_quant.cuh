@@ -1,0 +1,134 @@
+// e4m3 values with one fp32 scale per block of 128: activations per row and 128 columns, weights per 128 x 128 block.
+//
+// With top the largest magnitude of a block: scale = top / 448 (1 for a block of zeros), value = 448 x / top rounded to the
+// nearest e4m3 (ties to even). The quotient is decided exactly: x is a bf16 value, so 448 x is a whole number of at most 11
+// bits times a power of two and top one of 8 bits; their quotient either is a number of few bits (perhaps a tie between two
+// e4m3 values) or differs from every such number by more than 2^-17 of itself. A quotient q0 = a * (1 / m) corrected once by its
+// exactly computed remainder (a - q0 m, one fma) is within an ulp of a / m and is a / m itself where that is a fp32 number, so
+// the rounding to e4m3 comes out as that of the exact quotient. (Residual correction: Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990.)
+#pragma once
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int F8_BLOCK = 128;
+constexpr float F8_MAX = 448.f;
+
+struct F8Scaler {
+    float c, m, r, scale;
+    __device__ __forceinline__ explicit F8Scaler(float top) {
+        const bool some = top > 0.f;
+        // p = 2^k with top * p near 1 (its exponent kept where p, 448 p and 1 / (top p) are normal numbers)
+        const int e = min(max((int)(__float_as_uint(top) >> 23) & 255, 16), 252);
+        const float p = __uint_as_float((uint32_t)(254 - e) << 23);
+        c = p * F8_MAX;
+        m = some ? top * p : 1.f;
+        r = __frcp_rn(m);
+        scale = some ? __fdiv_rn(top, F8_MAX) : 1.f;
+    }
+    __device__ __forceinline__ float quotient(float x) const {
+        const float a = x * c;
+        const float q = a * r;
+        return fmaf(fmaf(-q, m, a), r, q);
+    }
+    __device__ __forceinline__ uint32_t pair(float x0, float x1) const {
+        return __nv_cvt_float2_to_fp8x2(make_float2(quotient(x0), quotient(x1)), __NV_SATFINITE, __NV_E4M3);
+    }
+    // 8 bf16 values -> 8 e4m3 bytes
+    __device__ __forceinline__ uint2 eight(const uint4& v) const {
+        const float2 f0 = unpack_bf16x2(v.x), f1 = unpack_bf16x2(v.y), f2 = unpack_bf16x2(v.z), f3 = unpack_bf16x2(v.w);
+        return make_uint2(pair(f0.x, f0.y) | pair(f1.x, f1.y) << 16, pair(f2.x, f2.y) | pair(f3.x, f3.y) << 16);
+    }
+};
+
+__device__ __forceinline__ float top_of(const uint4& v) {
+    const float2 f0 = unpack_bf16x2(v.x), f1 = unpack_bf16x2(v.y), f2 = unpack_bf16x2(v.z), f3 = unpack_bf16x2(v.w);
+    return fmaxf(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))),
+                 fmaxf(fmaxf(fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y))));
+}
+
+// Rows of x (row r of the output is row row_src[r] of x [T][K], or row r without row_src): q [R][K], s [ceil(K/128)][R].
+// A warp takes F8_CHUNK columns of a row; 16 lanes hold a block of 128. HBM-bound: 3 bytes moved per element.
+constexpr int F8_CHUNK_VEC = 128;  // 16-byte vectors of a work item: 4 per lane, loaded together
+
+__global__ void __launch_bounds__(256) fp8_row_quantize_kernel(const __nv_bfloat16* __restrict__ x,
+                                                               const int32_t* __restrict__ row_src, int T, int K, int R,
+                                                               uint8_t* __restrict__ q, float* __restrict__ s) {
+    grid_dep_wait();
+    grid_dep_trigger();
+    const int lane = threadIdx.x & 31;
+    const int nvec = K >> 3;
+    const int nchunk = (nvec + F8_CHUNK_VEC - 1) / F8_CHUNK_VEC;
+    const long items = (long)R * nchunk;
+    const long nwarps = (long)gridDim.x * (blockDim.x >> 5);
+    for (long it = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += nwarps) {
+        const int row = (int)(it / nchunk);
+        const int v0 = (int)(it - (long)row * nchunk) * F8_CHUNK_VEC + lane;
+        int src = row;
+        if (row_src) {
+            src = __ldg(row_src + row);
+            if (src < 0 || src >= T) {
+                if (lane == 0) flag_error(MOE_DEVERR_ROW_RANGE);
+                src = -1;
+            }
+        }
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (src >= 0 && v0 + 32 * i < nvec) v[i] = __ldg(reinterpret_cast<const uint4*>(x + (size_t)src * K) + v0 + 32 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float top = top_of(v[i]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (v0 + 32 * i >= nvec) continue;
+            const F8Scaler f(top);
+            *reinterpret_cast<uint2*>(q + (size_t)row * K + (size_t)(v0 + 32 * i) * 8) = f.eight(v[i]);
+            if ((lane & 15) == 0) s[(size_t)((v0 + 32 * i) >> 4) * R + row] = f.scale;
+        }
+    }
+}
+
+// Weights w [G][N][K]: one CTA per 128 x 128 block. q [G][N][K], s [G][ceil(N/128)][ceil(K/128)]. Once per layer.
+__global__ void __launch_bounds__(256) fp8_block_quantize_kernel(const __nv_bfloat16* __restrict__ w, int N, int K,
+                                                                 long blocks, uint8_t* __restrict__ q, float* __restrict__ s) {
+    __shared__ float red[2][8];
+    grid_dep_wait();
+    grid_dep_trigger();
+    const int kb = (K + F8_BLOCK - 1) / F8_BLOCK, nb = (N + F8_BLOCK - 1) / F8_BLOCK;
+    int turn = 0;
+    for (long b = blockIdx.x; b < blocks; b += gridDim.x, turn ^= 1) {
+        const int k0 = (int)(b % kb) * F8_BLOCK + (threadIdx.x & 15) * 8;
+        const long row0 = b / kb;
+        const long g = row0 / nb;
+        const int n0 = (int)(row0 - g * nb) * F8_BLOCK + (threadIdx.x >> 4);
+        uint4 v[8];
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (n0 + 16 * i < N && k0 < K)
+                v[i] = *reinterpret_cast<const uint4*>(w + ((size_t)g * N + n0 + 16 * i) * K + k0);
+            top = fmaxf(top, top_of(v[i]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, red[turn][i]);
+        const F8Scaler f(top);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (n0 + 16 * i < N && k0 < K)
+                *reinterpret_cast<uint2*>(q + ((size_t)g * N + n0 + 16 * i) * K + k0) = f.eight(v[i]);
+        if (threadIdx.x == 0) s[b] = f.scale;
+    }
+}
+
+}  // namespace moe

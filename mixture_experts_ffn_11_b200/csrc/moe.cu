@@ -22,6 +22,8 @@
 #include "gemm_swap.cuh"
 #include "gemm_fp4.cuh"
 #include "gemm_fp4_mma.cuh"
+#include "fp8_quant.cuh"
+#include "gemm_fp8.cuh"
 #include "gemm_wgrad.cuh"
 #include "backward.cuh"
 #include "combine.cuh"
@@ -158,6 +160,10 @@ cudaError_t set_gemm_attributes() {
         e = cudaFuncSetAttribute(grouped_gemm_fp4_warp_kernel<true>, a, GemmFp4WarpShape<true>::MAX_SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(grouped_gemm_fp4_warp_kernel<false>, a, GemmFp4WarpShape<false>::MAX_SMEM);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<true, 256>, a, Gemm8Shape<true, 256>::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<false, 256>, a, Gemm8Shape<false, 256>::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<true, 64>, a, Gemm8Shape<true, 64>::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<false, 64>, a, Gemm8Shape<false, 64>::SMEM_BYTES);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp4_kernel<16, true>, a, GemmFp4Shape<16, true>::SMEM_BYTES);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp4_kernel<32, true>, a, GemmFp4Shape<32, true>::SMEM_BYTES);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp4_kernel<64, true>, a, GemmFp4Shape<64, true>::SMEM_BYTES);
@@ -779,6 +785,86 @@ moe_status_t route_impl(const moe_bf16_t* x, const float* w_router, const moe_bf
     const cudaError_t e = launch_pdl(topk_kernel, dim3((T + TOPK_WARPS - 1) / TOPK_WARPS), dim3(TOPK_WARPS * 32), 0,
                                      stream, logits_out, T, E, k, (int)mode, topk_idx, topk_w);
     return check_launch("topk", e);
+}
+
+}  // namespace
+
+// ---- e4m3 operands with a scale per block of 128 ----
+namespace {
+
+template <bool GATEUP, int MAXN>
+moe_status_t launch_fp8(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, const int32_t* offsets, int G, int M,
+                        int d, int f, moe_bf16_t* out, int sms, cudaStream_t stream) {
+    using S = Gemm8Shape<GATEUP, MAXN>;
+    CUtensorMap tw, to;
+    Fp8Maps tx;
+    const int K = GATEUP ? d : f, n_out = GATEUP ? f : d;
+    const cuuint64_t k = (cuuint64_t)K, n = (cuuint64_t)n_out, g = (cuuint64_t)G;
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    moe_status_t st;
+    if (GATEUP) {  // [G][2][f][K] as [G][f/16][2][16][K]: one box = four times 16 gate rows and the 16 up rows of their columns
+        const cuuint64_t dims[5] = {k, 16, 2, n / 16, g};
+        const cuuint64_t str[4] = {k, n * k, 16 * k, 2 * n * k};
+        const cuuint32_t box[5] = {F8_BLOCK, 16, 2, 4, 1};
+        st = make_tmap(&tw, w, 5, dims, str, box, u8);
+    } else {
+        const cuuint64_t dims[3] = {k, n, g};
+        const cuuint64_t str[2] = {k, n * k};
+        const cuuint32_t box[3] = {F8_BLOCK, 128, 1};
+        st = make_tmap(&tw, w, 3, dims, str, box, u8);
+    }
+    const cuuint64_t xdims[2] = {k, (cuuint64_t)M};
+    const cuuint64_t xstr[1] = {k};
+    for (int i = 0; i < 4 && st == MOE_OK; ++i) {
+        const cuuint32_t box[2] = {F8_BLOCK, (cuuint32_t)(128 >> i)};
+        st = make_tmap(&tx.x[i], a, 2, xdims, xstr, box, u8);
+    }
+    if (st == MOE_OK) {  // 32 tokens x the columns of one warp
+        const cuuint64_t dims[2] = {n, (cuuint64_t)M};
+        const cuuint64_t str[1] = {n * 2};
+        const cuuint32_t box[2] = {GATEUP ? 16 : 32, 32};
+        st = make_tmap(&to, out, 2, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       GATEUP ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B);
+    }
+    if (st != MOE_OK) return st;
+    Gemm8Args args;
+    args.group_offsets = offsets;
+    args.sa = sa;
+    args.sw = sw;
+    args.G = G;
+    args.M = M;
+    args.K = K;
+    args.n_out = n_out;
+    args.wblocks = (n_out + S::TILE_W - 1) / S::TILE_W;
+    args.out = reinterpret_cast<__nv_bfloat16*>(out);
+    const long upper = ((long)M / MAXN + G) * (long)args.wblocks;  // >= the real tile count
+    const int clusters = (int)(upper < sms / 2 ? upper : sms / 2);
+    const int streamed_once = (long)M <= (long)G * MAXN ? 1 : 0;
+    const cudaError_t e = launch_pdl(grouped_gemm_fp8_kernel<GATEUP, MAXN>, dim3(2 * clusters), dim3(G8_THREADS), S::SMEM_BYTES,
+                                     stream, tw, tx, to, args, streamed_once);
+    return check_launch(GATEUP ? "grouped_gemm_gateup_fp8" : "grouped_gemm_down_fp8", e);
+}
+
+// Arguments of both products, then the launch: tiles of up to 256 token rows, or of 64 when the groups average at most 48.
+template <bool GATEUP>
+moe_status_t gemm_fp8(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, const int32_t* offsets, int G, int M,
+                      int d, int f, moe_bf16_t* out, cudaStream_t stream) {
+    if (!w || !sw || !offsets || (M > 0 && (!a || !sa || !out))) return fail(MOE_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned16(a) || !aligned16(w) || !aligned16(out))
+        return fail(MOE_ERR_INVALID_ARG, "value and output pointers must be 16-byte aligned");
+    if (((reinterpret_cast<uintptr_t>(offsets) | reinterpret_cast<uintptr_t>(sa) | reinterpret_cast<uintptr_t>(sw)) & 3u) != 0)
+        return fail(MOE_ERR_INVALID_ARG, "offsets or scales misaligned");
+    if (G < 1 || G > GG_MAX_GROUPS) return fail(MOE_ERR_INVALID_ARG, "G=%d outside [1, %d]", G, GG_MAX_GROUPS);
+    if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M=%d < 0", M);
+    if (d < 16 || f < 16 || d % 16 || f % 16)
+        return fail(MOE_ERR_INVALID_ARG, "d=%d and f=%d must be positive multiples of 16 (16-byte rows of e4m3)", d, f);
+    DeviceInfo di;
+    moe_status_t st = device_info(di);
+    if (st != MOE_OK) return st;
+    if (di.sms < 2) return fail(MOE_ERR_UNSUPPORTED, "the fp8 GEMM needs CTA pairs");
+    if (M == 0) return MOE_OK;
+    if ((long)M <= 48L * G) return launch_fp8<GATEUP, 64>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
+    return launch_fp8<GATEUP, 256>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
 }
 
 }  // namespace
@@ -1428,6 +1514,55 @@ moe_status_t moe_router_backward(const moe_bf16_t* x, const float* w_router, con
                    (const float*)dl_tk, w_router, reinterpret_cast<const __nv_bfloat16*>(dx_addend), T, d, E, k,
                    reinterpret_cast<__nv_bfloat16*>(dx));
     return check_launch("router_input_grad", e);
+}
+
+// ---- e4m3 operands with a scale per block of 128 ----
+
+moe_status_t moe_fp8_block_quantize(const moe_bf16_t* w, int G, int N, int K, uint8_t* q, float* s, cudaStream_t stream) {
+    if (G < 0 || N < 0) return fail(MOE_ERR_INVALID_ARG, "G=%d or N=%d < 0", G, N);
+    if (K < 16 || K % 16) return fail(MOE_ERR_INVALID_ARG, "K=%d must be a positive multiple of 16", K);
+    if (G == 0 || N == 0) return MOE_OK;
+    if (!w || !q || !s) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(w) || !aligned16(q) || (reinterpret_cast<uintptr_t>(s) & 3u) != 0)
+        return fail(MOE_ERR_INVALID_ARG, "w and q must be 16-byte, s 4-byte aligned");
+    DeviceInfo di;
+    moe_status_t st = device_info(di);
+    if (st != MOE_OK) return st;
+    const long blocks = (long)G * ((N + F8_BLOCK - 1) / F8_BLOCK) * ((K + F8_BLOCK - 1) / F8_BLOCK);
+    return check_launch("fp8_block_quantize",
+                        launch_pdl(fp8_block_quantize_kernel, dim3(grid_cap(blocks, di.sms, 6)), dim3(256), 0, stream,
+                                   reinterpret_cast<const __nv_bfloat16*>(w), N, K, blocks, q, s));
+}
+
+moe_status_t moe_fp8_row_quantize(const moe_bf16_t* x, const int32_t* row_src, int T, int K, int R, uint8_t* q, float* s,
+                                  cudaStream_t stream) {
+    if (T < 0 || R < 0) return fail(MOE_ERR_INVALID_ARG, "T=%d or R=%d < 0", T, R);
+    if (K < 16 || K % 16) return fail(MOE_ERR_INVALID_ARG, "K=%d must be a positive multiple of 16", K);
+    if (!row_src && R > T) return fail(MOE_ERR_INVALID_ARG, "R=%d rows of T=%d without row_src", R, T);
+    if (R == 0) return MOE_OK;
+    if (T == 0 || !x || !q || !s) return fail(MOE_ERR_INVALID_ARG, "no source rows, or null pointer");
+    if (!aligned16(x) || !aligned16(q) ||
+        ((reinterpret_cast<uintptr_t>(row_src) | reinterpret_cast<uintptr_t>(s)) & 3u) != 0)
+        return fail(MOE_ERR_INVALID_ARG, "x and q must be 16-byte, row_src and s 4-byte aligned");
+    DeviceInfo di;
+    moe_status_t st = device_info(di);
+    if (st != MOE_OK) return st;
+    const long items = (long)R * ((K / 8 + F8_CHUNK_VEC - 1) / F8_CHUNK_VEC);
+    return check_launch("fp8_row_quantize",
+                        launch_pdl(fp8_row_quantize_kernel, dim3(grid_cap((items + 7) / 8, di.sms, 8)), dim3(256), 0, stream,
+                                   reinterpret_cast<const __nv_bfloat16*>(x), row_src, T, K, R, q, s));
+}
+
+moe_status_t moe_grouped_gemm_gateup_fp8(const uint8_t* aq, const float* as, const uint8_t* wq_gateup, const float* ws_gateup,
+                                         const int32_t* group_offsets, int G, int M, int d, int f, moe_bf16_t* h,
+                                         cudaStream_t stream) {
+    return gemm_fp8<true>(aq, as, wq_gateup, ws_gateup, group_offsets, G, M, d, f, h, stream);
+}
+
+moe_status_t moe_grouped_gemm_down_fp8(const uint8_t* hq, const float* hs, const uint8_t* wq_down, const float* ws_down,
+                                       const int32_t* group_offsets, int G, int M, int d, int f, moe_bf16_t* y,
+                                       cudaStream_t stream) {
+    return gemm_fp8<false>(hq, hs, wq_down, ws_down, group_offsets, G, M, d, f, y, stream);
 }
 
 // ---- block norms ----
