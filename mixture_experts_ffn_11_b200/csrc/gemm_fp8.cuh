@@ -13,7 +13,9 @@
 //               token rows (one box); completion is counted on the leader's full[stage].
 //   warp 1      TMEM allocation; in the leader the MMA issuer: per K block four MMAs (K = 32 each) into the next of NBUF
 //               TMEM buffers, so the tensor cores run ahead of the warps that read them.
-//   warps 2, 3  scale loaders, alternating K blocks: sa of the tile's tokens times sw of this CTA's weight rows, into a ring.
+//   warps 2, 3  scales: sa of the tile's tokens and sw of this CTA's weight rows into a ring by asynchronous copies (warp 2),
+//               their products into another (warp 3). (Loaded through registers two K blocks ahead, the loads' latency set the
+//               pace: 1.2 us per K block at any tile size.)
 //   warps 4-11  two warpgroups, each the four lane quarters of half the tile's tokens: read a K block's sums from TMEM
 //               (tcgen05.ld 16x256b: the layout of an MMA fragment, thread = 2 rows x 2 tokens of each 16 x 8 block),
 //               multiply by the scales, add to the tile's sums in registers (MAXN / 2 per thread); after the last K block
@@ -31,7 +33,8 @@
 namespace moe {
 
 constexpr int G8_THREADS = 384;
-constexpr int G8_SCALE_STAGES = 6;
+constexpr int G8_SCALE_STAGES = 4;  // ring of products sa * sw
+constexpr int G8_RAW_STAGES = 8;    // ring of scales as they arrive from memory
 
 struct Gemm8Args {
     const int32_t* group_offsets;  // [G+1], device
@@ -50,14 +53,16 @@ struct Gemm8Shape {
     static constexpr int NBUF = 512 / MAXN;
     static constexpr int TILE_W = GATEUP ? 128 : 256;
     static constexpr int SCALE_BYTES = (GATEUP ? 2 : 1) * MAXN * 4;
+    static constexpr int RAW_FLOATS = MAXN + 4;
     static constexpr int EPI_BYTES = 8 * 2 * 2048;  // two staging blocks per warp
     static constexpr int BAR_BYTES = 512;
     static constexpr int TABLE_BYTES = (2 * (GG_MAX_GROUPS + 1) * 4 + 127) / 128 * 128;
     static constexpr int SMEM_BYTES =
-        1024 + STAGES * STAGE_BYTES + EPI_BYTES + G8_SCALE_STAGES * SCALE_BYTES + BAR_BYTES + TABLE_BYTES;
+        1024 + STAGES * STAGE_BYTES + EPI_BYTES + G8_SCALE_STAGES * SCALE_BYTES +
+        G8_RAW_STAGES * RAW_FLOATS * 4 + BAR_BYTES + TABLE_BYTES;
     static_assert(STAGE_BYTES % 1024 == 0, "stage bases stay 1024-byte aligned");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
-    static_assert((2 * STAGES + 2 * NBUF + 2 * G8_SCALE_STAGES + 2) * 8 + 8 <= BAR_BYTES, "barrier area");
+    static_assert((2 * STAGES + 2 * NBUF + 2 * G8_SCALE_STAGES + 2 * G8_RAW_STAGES + 2) * 8 + 8 <= BAR_BYTES, "barrier area");
 };
 
 // token boxes of 128, 64, 32, 16 rows
@@ -98,6 +103,16 @@ __device__ __forceinline__ void tmem_wait_ld(float (&a)[8], float (&b)[8]) {
                  :
                  : "memory");
 }
+
+// Asynchronous copy of one float (zero where `inside` is false: nothing is read), and an arrival on `bar` once every such copy
+// of this thread so far has landed (counted among the barrier's expected arrivals).
+__device__ __forceinline__ void cp_async_f32(float* dst, const float* src, bool inside) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(inside ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_mbar_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Four 8 x 8 blocks of 16-bit elements, each stored transposed: lane 8 m + i gives the address of row i of block m.
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -142,13 +157,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
     uint8_t* stages = smem;
     uint8_t* epi = smem + STAGES * S::STAGE_BYTES;
     uint8_t* scales = epi + S::EPI_BYTES;
-    uint64_t* full_bar = reinterpret_cast<uint64_t*>(scales + G8_SCALE_STAGES * S::SCALE_BYTES);  // used in the leader
+    float* raw = reinterpret_cast<float*>(scales + G8_SCALE_STAGES * S::SCALE_BYTES);
+    uint64_t* full_bar = reinterpret_cast<uint64_t*>(raw + G8_RAW_STAGES * S::RAW_FLOATS);  // used in the leader
     uint64_t* empty_bar = full_bar + STAGES;
     uint64_t* tfull_bar = empty_bar + STAGES;  // [NBUF]
     uint64_t* tempty_bar = tfull_bar + NBUF;   // [NBUF], used in the leader
     uint64_t* sfull_bar = tempty_bar + NBUF;   // [G8_SCALE_STAGES]
     uint64_t* sempty_bar = sfull_bar + G8_SCALE_STAGES;
-    uint64_t* final_bar = sempty_bar + G8_SCALE_STAGES;
+    uint64_t* rfull_bar = sempty_bar + G8_SCALE_STAGES;  // [G8_RAW_STAGES]
+    uint64_t* rempty_bar = rfull_bar + G8_RAW_STAGES;
+    uint64_t* final_bar = rempty_bar + G8_RAW_STAGES;
     uint64_t* never_bar = final_bar + 1;  // nothing arrives on it (test_stall)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(never_bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -175,6 +193,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         for (int s = 0; s < G8_SCALE_STAGES; ++s) {
             mbar_init(&sfull_bar[s], 32);
             mbar_init(&sempty_bar[s], 8);
+        }
+        for (int s = 0; s < G8_RAW_STAGES; ++s) {
+            mbar_init(&rfull_bar[s], 32);
+            mbar_init(&rempty_bar[s], 32);
         }
         mbar_init(final_bar, 1);
         mbar_init(never_bar, 1);
@@ -228,6 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
     tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
     const int total = s_tp[G];
+    const uint64_t limit = wait_limit_ns();
 
     // tile -> group g, weight block wb, first token row r0 (absolute), rows in the tile (<= MAXN)
     auto locate = [&](int tile, int& g, int& wb, int& r0, int& rows) {
@@ -266,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             const uint32_t tx = 2u * (uint32_t)(S::W_BYTES + (128 >> bi) * F8_BLOCK);
             for (int kb = 0; kb < KB; ++kb) {
                 if (lane == 0) {
-                    ok = mbar_wait_bounded(&empty_bar[stage], phase ^ 1u, abort_flag);
+                    ok = mbar_wait_within(&empty_bar[stage], phase ^ 1u, abort_flag, limit);
                     if (ok) {
                         uint8_t* sw = stages + stage * S::STAGE_BYTES;
                         const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
@@ -307,8 +330,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                 const uint32_t idesc = idesc_e4m3_f32(256, (rows + 31) / 32 * 32);
                 for (int kb = 0; kb < KB; ++kb) {
                     if (lane == 0) {
-                        ok = mbar_wait_bounded(&tempty_bar[buf], buf_phase ^ 1u, abort_flag) &&
-                             mbar_wait_bounded(&full_bar[stage], phase, abort_flag);
+                        ok = mbar_wait_within(&tempty_bar[buf], buf_phase ^ 1u, abort_flag, limit) &&
+                             mbar_wait_within(&full_bar[stage], phase, abort_flag, limit);
                         if (ok) {
                             tc_fence_after_sync();
                             const uint32_t sa = smem_u32(stages + stage * S::STAGE_BYTES);
@@ -337,59 +360,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             __syncwarp();
         }
     } else if (warp < 4) {
-        // ---------------- scale loaders (both CTAs): steps (tile, K block) of parity warp - 2 ----------------
+        // ---------------- scales (both CTAs) ----------------
+        // warp 2: raw scales of each step (tile, K block) into a ring, by asynchronous 4-byte copies (rows start anywhere):
+        // sa of the tile's tokens, then the one or two sw of this CTA's weight rows. Nothing waits for a copy here, so a ring's
+        // depth of them is in flight. warp 3: their products into the ring the sums read.
         constexpr int PER = MAXN / 32;
-        const int KBW = KB;
         const int nblk = (args.n_out + F8_BLOCK - 1) / F8_BLOCK;
-        int slot = 0;
-        uint32_t phase = 0;
+        int slot = 0, cslot = 0;
+        uint32_t phase = 0, c_phase = 0;
         bool ok = true;
-        int step = 0;
         for (int tile = cluster; tile < total && ok; tile += n_clusters) {
             int g, wb, r0, rows;
             locate(tile, g, wb, r0, rows);
-            // weight scales of this CTA's rows, by K block: gate|up has one row of blocks for the gate and one for the up rows
-            const float* w0;
-            const float* w1 = nullptr;
-            if constexpr (GATEUP) {
-                w0 = args.sw + ((size_t)g * 2 * nblk + wb) * KBW;
-                w1 = w0 + (size_t)nblk * KBW;
-            } else {
-                w0 = args.sw + ((size_t)g * nblk + min(2 * wb + (int)rank, nblk - 1)) * KBW;
-            }
-            const float* a0 = args.sa + r0;
-            int kb = (step ^ (warp - 2)) & 1;  // first K block of this warp's parity
-            float a[PER], b0 = 0.f, b1 = 0.f;
-            auto fetch = [&](int k) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int t = lane + 32 * i;
-                    a[i] = t < rows ? __ldg(a0 + (size_t)k * args.M + t) : 0.f;
-                }
-                b0 = __ldg(w0 + k);
-                if constexpr (GATEUP) b1 = __ldg(w1 + k);
-            };
-            if (kb < KB) fetch(kb);
-            for (int k = 0; k < KB; ++k, ++step) {
-                if (((step ^ (warp - 2)) & 1) == 0) {
-                    float* to = reinterpret_cast<float*>(scales + slot * S::SCALE_BYTES);
-                    ok = mbar_wait_bounded(&sempty_bar[slot], phase ^ 1u, abort_flag);
+            if (warp == 2) {
+                const float* w0;
+                if constexpr (GATEUP)
+                    w0 = args.sw + (((size_t)g * 2 + (lane & 1)) * nblk + wb) * KB;
+                else
+                    w0 = args.sw + ((size_t)g * nblk + min(2 * wb + (int)rank, nblk - 1)) * KB;
+                const float* a0 = args.sa + r0;
+                for (int kb = 0; kb < KB; ++kb) {
+                    ok = mbar_wait_within(&rempty_bar[slot], phase ^ 1u, abort_flag, limit);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
+                    float* to = raw + slot * S::RAW_FLOATS;
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
-                        to[lane + 32 * i] = a[i] * b0;
-                        if constexpr (GATEUP) to[MAXN + lane + 32 * i] = a[i] * b1;
+                        const int t = lane + 32 * i;
+                        cp_async_f32(to + t, a0 + (size_t)kb * args.M + (t < rows ? t : 0), t < rows);
                     }
-                    mbar_arrive(&sfull_bar[slot]);
-                    if (k + 2 < KB) fetch(k + 2);
+                    if (lane < 2) cp_async_f32(to + MAXN + lane, w0 + kb, true);
+                    cp_async_mbar_arrive(&rfull_bar[slot]);
+                    if (++slot == G8_RAW_STAGES) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (++slot == G8_SCALE_STAGES) {
-                    slot = 0;
-                    phase ^= 1u;
+            } else {
+                for (int kb = 0; kb < KB; ++kb) {
+                    ok = mbar_wait_within(&rfull_bar[slot], phase, abort_flag, limit) &&
+                         mbar_wait_within(&sempty_bar[cslot], c_phase ^ 1u, abort_flag, limit);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const float* from = raw + slot * S::RAW_FLOATS;
+                    float* to = reinterpret_cast<float*>(scales + cslot * S::SCALE_BYTES);
+                    const float b0 = from[MAXN], b1 = from[MAXN + 1];
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const float a = from[lane + 32 * i];
+                        to[lane + 32 * i] = a * b0;
+                        if constexpr (GATEUP) to[MAXN + lane + 32 * i] = a * b1;
+                    }
+                    mbar_arrive(&rempty_bar[slot]);
+                    mbar_arrive(&sfull_bar[cslot]);
+                    if (++slot == G8_RAW_STAGES) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                    if (++cslot == G8_SCALE_STAGES) {
+                        cslot = 0;
+                        c_phase ^= 1u;
+                    }
                 }
             }
         }
+        if (warp == 2) cp_async_wait_all();  // no copy is in flight when the CTA leaves
+        __syncwarp();
     } else {
         // ---------------- scaled sums and epilogue (warps 4-11, both CTAs) ----------------
         constexpr int CHUNKS = MAXN / 32;  // 16-token chunks of this warpgroup's half
@@ -410,8 +446,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                 for (int i = 0; i < 8; ++i) acc[c][0][i] = acc[c][1][i] = 0.f;
             for (int kb = 0; kb < KB; ++kb) {
                 if (lane == 0)
-                    ok = mbar_wait_bounded(&sfull_bar[slot], s_phase, abort_flag) &&
-                         mbar_wait_bounded(&tfull_bar[buf], buf_phase, abort_flag);
+                    ok = mbar_wait_within(&sfull_bar[slot], s_phase, abort_flag, limit) &&
+                         mbar_wait_within(&tfull_bar[buf], buf_phase, abort_flag, limit);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 tc_fence_after_sync();
@@ -442,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
+                    mbar_arrive_remote(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
                     mbar_arrive(&sempty_bar[slot]);
                 }
                 if (++buf == NBUF) {

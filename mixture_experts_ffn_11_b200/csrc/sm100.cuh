@@ -132,6 +132,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The same without cluster-scope release semantics (which cost a memory barrier of about 2000 cycles): for signals that order
+// nothing but this thread's completed tensor-memory loads (tcgen05.wait::ld, then tcgen05.fence::before_thread_sync).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // TMA loads issued by either CTA of a pair whose completion is counted on an mbarrier of the pair's
 // first CTA (bar_cluster_addr is a shared::cluster address). Plain loads: no multicast.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster_addr,
