@@ -25,6 +25,8 @@
 // What bounds it: many rows, the tensor cores (at 256 tokens a K block takes 512 cycles of MMA; reading it back takes 256
 // cycles of TMEM bandwidth and 256 of FMA, beside it); few rows, HBM (weights streamed once).
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp8_quant.cuh"
 #include "gemm.cuh"
@@ -86,22 +88,46 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Start loading 16 lanes x 16 columns of fp32 from TMEM. Thread t gets, for each block j of 8 columns, lane t / 4 and
+// Start loading 16 lanes x 32 columns of fp32 from TMEM. Thread t gets, for each block j of 8 columns, lane t / 4 and
 // columns 2 (t % 4), + 1 in r[4j], r[4j + 1], and lane t / 4 + 8 in r[4j + 2], r[4j + 3]. The registers are valid after
 // tmem_wait_ld on them.
-__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, float (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
-                 : "r"(taddr)
-                 : "memory");
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr)
+        : "memory");
 }
 // Wait for this warp's TMEM loads; the registers they write pass through, so nothing reads them earlier.
-__device__ __forceinline__ void tmem_wait_ld(float (&a)[8], float (&b)[8]) {
+__device__ __forceinline__ void tmem_wait_ld(float (&a)[16], float (&b)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(a[4]), "+f"(a[5]), "+f"(a[6]), "+f"(a[7]),
-                   "+f"(b[0]), "+f"(b[1]), "+f"(b[2]), "+f"(b[3]), "+f"(b[4]), "+f"(b[5]), "+f"(b[6]), "+f"(b[7])
+                 : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(a[4]), "+f"(a[5]), "+f"(a[6]), "+f"(a[7]), "+f"(a[8]),
+                   "+f"(a[9]), "+f"(a[10]), "+f"(a[11]), "+f"(a[12]), "+f"(a[13]), "+f"(a[14]), "+f"(a[15]), "+f"(b[0]),
+                   "+f"(b[1]), "+f"(b[2]), "+f"(b[3]), "+f"(b[4]), "+f"(b[5]), "+f"(b[6]), "+f"(b[7]), "+f"(b[8]), "+f"(b[9]),
+                   "+f"(b[10]), "+f"(b[11]), "+f"(b[12]), "+f"(b[13]), "+f"(b[14]), "+f"(b[15])
                  :
                  : "memory");
+}
+
+// acc += {v0, v1} * s, two fp32 multiply-adds in one instruction
+__device__ __forceinline__ void fma2(float2& acc, float v0, float v1, const float2& s) {
+    asm("{\n\t.reg .b64 a, v, s;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\t"
+        "fma.rn.f32x2 a, v, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y)
+        : "f"(v0), "f"(v1), "f"(s.x), "f"(s.y));
+}
+
+// Register shares of the warpgroups (setmaxnreg): the block is launched with 384 x 168 = 64,512 registers, which the
+// 128 x 72 of warps 0-3 and the 256 x 216 of the others use up exactly.
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 // Asynchronous copy of one float (zero where `inside` is false: nothing is read), and an arrival on `bar` once every such copy
@@ -272,162 +298,166 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         rows = min(MAXN, n - ti * MAXN);
     };
 
-    if (warp == 0) {
-        // ---------------- TMA producer (both CTAs) ----------------
-        const uint64_t pol_x = l2_policy_evict_last();
-        const uint64_t pol_w = weights_streamed_once ? l2_policy_evict_first() : l2_policy_evict_normal();
-        int stage = 0;
-        uint32_t phase = 0;
-        long issued = 0;
-        bool ok = true;
-        for (int tile = cluster; tile < total && ok; tile += n_clusters) {
-            int g, wb, r0, rows;
-            locate(tile, g, wb, r0, rows);
-            const int half = (rows + 31) / 32 * 16;  // token rows per CTA (N / 2)
-            const int bi = swap_box_index(half);
-            const int xrow0 = r0 + (int)rank * half;
-            const uint32_t tx = 2u * (uint32_t)(S::W_BYTES + (128 >> bi) * F8_BLOCK);
-            for (int kb = 0; kb < KB; ++kb) {
-                if (lane == 0) {
-                    ok = mbar_wait_within(&empty_bar[stage], phase ^ 1u, abort_flag, limit);
-                    if (ok) {
-                        uint8_t* sw = stages + stage * S::STAGE_BYTES;
-                        const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
-                        if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
-                        if constexpr (GATEUP)
-                            tma_load_5d_pair(sw, &tmW, bar, kb * F8_BLOCK, 0, 0, wb * 8 + 4 * (int)rank, g, pol_w);
-                        else
-                            tma_load_3d_pair(sw, &tmW, bar, kb * F8_BLOCK, wb * 256 + 128 * (int)rank, g, pol_w);
-                        tma_load_2d_pair(sw + S::W_BYTES, &tmX.x[bi], bar, kb * F8_BLOCK, xrow0, pol_x);
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                ++issued;
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        // the leader's full barriers count both CTAs' copies: it waits for the last ones (bounded)
-        if (lane == 0 && leader) {
-            for (long n = issued > STAGES ? issued - STAGES : 0; n < issued; ++n)
-                mbar_wait_drain(&full_bar[n % STAGES], (uint32_t)((n / STAGES) & 1));
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------- MMA issuer (leader only) ----------------
-        if (leader) {
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
+    if (warp < 4) {
+        if constexpr (MAXN == 256) fewer_registers<72>();
+        if (warp == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            const uint64_t pol_x = l2_policy_evict_last();
+            const uint64_t pol_w = weights_streamed_once ? l2_policy_evict_first() : l2_policy_evict_normal();
+            int stage = 0;
+            uint32_t phase = 0;
+            long issued = 0;
             bool ok = true;
-            if (lane == 0) ok = test_stall(never_bar, abort_flag);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
             for (int tile = cluster; tile < total && ok; tile += n_clusters) {
                 int g, wb, r0, rows;
                 locate(tile, g, wb, r0, rows);
-                const uint32_t idesc = idesc_e4m3_f32(256, (rows + 31) / 32 * 32);
+                const int half = (rows + 31) / 32 * 16;  // token rows per CTA (N / 2)
+                const int bi = swap_box_index(half);
+                const int xrow0 = r0 + (int)rank * half;
+                const uint32_t tx = 2u * (uint32_t)(S::W_BYTES + (128 >> bi) * F8_BLOCK);
                 for (int kb = 0; kb < KB; ++kb) {
                     if (lane == 0) {
-                        ok = mbar_wait_within(&tempty_bar[buf], buf_phase ^ 1u, abort_flag, limit) &&
-                             mbar_wait_within(&full_bar[stage], phase, abort_flag, limit);
+                        ok = mbar_wait_within(&empty_bar[stage], phase ^ 1u, abort_flag, limit);
                         if (ok) {
-                            tc_fence_after_sync();
-                            const uint32_t sa = smem_u32(stages + stage * S::STAGE_BYTES);
-                            const uint64_t wdesc = smem_desc_sw128(sa), xdesc = smem_desc_sw128(sa + S::W_BYTES);
-                            const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAXN);
-#pragma unroll
-                            for (int k = 0; k < F8_BLOCK / 32; ++k)
-                                umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
-                            umma_commit_pair_multicast(&empty_bar[stage], 0x3);
-                            umma_commit_pair_multicast(&tfull_bar[buf], 0x3);
+                            uint8_t* sw = stages + stage * S::STAGE_BYTES;
+                            const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+                            if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
+                            if constexpr (GATEUP)
+                                tma_load_5d_pair(sw, &tmW, bar, kb * F8_BLOCK, 0, 0, wb * 8 + 4 * (int)rank, g, pol_w);
+                            else
+                                tma_load_3d_pair(sw, &tmW, bar, kb * F8_BLOCK, wb * 256 + 128 * (int)rank, g, pol_w);
+                            tma_load_2d_pair(sw + S::W_BYTES, &tmX.x[bi], bar, kb * F8_BLOCK, xrow0, pol_x);
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) break;
+                    ++issued;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (++buf == NBUF) {
-                        buf = 0;
-                        buf_phase ^= 1u;
+                }
+            }
+            // the leader's full barriers count both CTAs' copies: it waits for the last ones (bounded)
+            if (lane == 0 && leader) {
+                for (long n = issued > STAGES ? issued - STAGES : 0; n < issued; ++n)
+                    mbar_wait_drain(&full_bar[n % STAGES], (uint32_t)((n / STAGES) & 1));
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ---------------- MMA issuer (leader only) ----------------
+            if (leader) {
+                int stage = 0, buf = 0;
+                uint32_t phase = 0, buf_phase = 0;
+                bool ok = true;
+                if (lane == 0) ok = test_stall(never_bar, abort_flag);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                for (int tile = cluster; tile < total && ok; tile += n_clusters) {
+                    int g, wb, r0, rows;
+                    locate(tile, g, wb, r0, rows);
+                    const uint32_t idesc = idesc_e4m3_f32(256, (rows + 31) / 32 * 32);
+                    for (int kb = 0; kb < KB; ++kb) {
+                        if (lane == 0) {
+                            ok = mbar_wait_within(&tempty_bar[buf], buf_phase ^ 1u, abort_flag, limit) &&
+                                 mbar_wait_within(&full_bar[stage], phase, abort_flag, limit);
+                            if (ok) {
+                                tc_fence_after_sync();
+                                const uint32_t sa = smem_u32(stages + stage * S::STAGE_BYTES);
+                                const uint64_t wdesc = smem_desc_sw128(sa), xdesc = smem_desc_sw128(sa + S::W_BYTES);
+                                const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAXN);
+#pragma unroll
+                                for (int k = 0; k < F8_BLOCK / 32; ++k)
+                                    umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
+                                umma_commit_pair_multicast(&empty_bar[stage], 0x3);
+                                umma_commit_pair_multicast(&tfull_bar[buf], 0x3);
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        if (++buf == NBUF) {
+                            buf = 0;
+                            buf_phase ^= 1u;
+                        }
+                    }
+                }
+                if (lane == 0) umma_commit_pair(final_bar);
+                __syncwarp();
+            }
+        } else {
+            // ---------------- scales (both CTAs) ----------------
+            // warp 2: raw scales of each step (tile, K block) into a ring, by asynchronous 4-byte copies (rows start anywhere):
+            // sa of the tile's tokens, then the one or two sw of this CTA's weight rows. Nothing waits for a copy here, so a ring's
+            // depth of them is in flight. warp 3: their products into the ring the sums read.
+            constexpr int PER = MAXN / 32;
+            const int nblk = (args.n_out + F8_BLOCK - 1) / F8_BLOCK;
+            int slot = 0, cslot = 0;
+            uint32_t phase = 0, c_phase = 0;
+            bool ok = true;
+            for (int tile = cluster; tile < total && ok; tile += n_clusters) {
+                int g, wb, r0, rows;
+                locate(tile, g, wb, r0, rows);
+                if (warp == 2) {
+                    const float* w0;
+                    if constexpr (GATEUP)
+                        w0 = args.sw + (((size_t)g * 2 + (lane & 1)) * nblk + wb) * KB;
+                    else
+                        w0 = args.sw + ((size_t)g * nblk + min(2 * wb + (int)rank, nblk - 1)) * KB;
+                    const float* a0 = args.sa + r0;
+                    for (int kb = 0; kb < KB; ++kb) {
+                        ok = mbar_wait_within(&rempty_bar[slot], phase ^ 1u, abort_flag, limit);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        float* to = raw + slot * S::RAW_FLOATS;
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const int t = lane + 32 * i;
+                            cp_async_f32(to + t, a0 + (size_t)kb * args.M + (t < rows ? t : 0), t < rows);
+                        }
+                        if (lane < 2) cp_async_f32(to + MAXN + lane, w0 + kb, true);
+                        cp_async_mbar_arrive(&rfull_bar[slot]);
+                        if (++slot == G8_RAW_STAGES) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                } else {
+                    for (int kb = 0; kb < KB; ++kb) {
+                        ok = mbar_wait_within(&rfull_bar[slot], phase, abort_flag, limit) &&
+                             mbar_wait_within(&sempty_bar[cslot], c_phase ^ 1u, abort_flag, limit);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const float* from = raw + slot * S::RAW_FLOATS;
+                        float* to = reinterpret_cast<float*>(scales + cslot * S::SCALE_BYTES);
+                        const float b0 = from[MAXN], b1 = from[MAXN + 1];
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const float a = from[lane + 32 * i];
+                            to[lane + 32 * i] = a * b0;
+                            if constexpr (GATEUP) to[MAXN + lane + 32 * i] = a * b1;
+                        }
+                        mbar_arrive(&rempty_bar[slot]);
+                        mbar_arrive(&sfull_bar[cslot]);
+                        if (++slot == G8_RAW_STAGES) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                        if (++cslot == G8_SCALE_STAGES) {
+                            cslot = 0;
+                            c_phase ^= 1u;
+                        }
                     }
                 }
             }
-            if (lane == 0) umma_commit_pair(final_bar);
+            if (warp == 2) cp_async_wait_all();  // no copy is in flight when the CTA leaves
             __syncwarp();
         }
-    } else if (warp < 4) {
-        // ---------------- scales (both CTAs) ----------------
-        // warp 2: raw scales of each step (tile, K block) into a ring, by asynchronous 4-byte copies (rows start anywhere):
-        // sa of the tile's tokens, then the one or two sw of this CTA's weight rows. Nothing waits for a copy here, so a ring's
-        // depth of them is in flight. warp 3: their products into the ring the sums read.
-        constexpr int PER = MAXN / 32;
-        const int nblk = (args.n_out + F8_BLOCK - 1) / F8_BLOCK;
-        int slot = 0, cslot = 0;
-        uint32_t phase = 0, c_phase = 0;
-        bool ok = true;
-        for (int tile = cluster; tile < total && ok; tile += n_clusters) {
-            int g, wb, r0, rows;
-            locate(tile, g, wb, r0, rows);
-            if (warp == 2) {
-                const float* w0;
-                if constexpr (GATEUP)
-                    w0 = args.sw + (((size_t)g * 2 + (lane & 1)) * nblk + wb) * KB;
-                else
-                    w0 = args.sw + ((size_t)g * nblk + min(2 * wb + (int)rank, nblk - 1)) * KB;
-                const float* a0 = args.sa + r0;
-                for (int kb = 0; kb < KB; ++kb) {
-                    ok = mbar_wait_within(&rempty_bar[slot], phase ^ 1u, abort_flag, limit);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    float* to = raw + slot * S::RAW_FLOATS;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const int t = lane + 32 * i;
-                        cp_async_f32(to + t, a0 + (size_t)kb * args.M + (t < rows ? t : 0), t < rows);
-                    }
-                    if (lane < 2) cp_async_f32(to + MAXN + lane, w0 + kb, true);
-                    cp_async_mbar_arrive(&rfull_bar[slot]);
-                    if (++slot == G8_RAW_STAGES) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
-                }
-            } else {
-                for (int kb = 0; kb < KB; ++kb) {
-                    ok = mbar_wait_within(&rfull_bar[slot], phase, abort_flag, limit) &&
-                         mbar_wait_within(&sempty_bar[cslot], c_phase ^ 1u, abort_flag, limit);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const float* from = raw + slot * S::RAW_FLOATS;
-                    float* to = reinterpret_cast<float*>(scales + cslot * S::SCALE_BYTES);
-                    const float b0 = from[MAXN], b1 = from[MAXN + 1];
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const float a = from[lane + 32 * i];
-                        to[lane + 32 * i] = a * b0;
-                        if constexpr (GATEUP) to[MAXN + lane + 32 * i] = a * b1;
-                    }
-                    mbar_arrive(&rempty_bar[slot]);
-                    mbar_arrive(&sfull_bar[cslot]);
-                    if (++slot == G8_RAW_STAGES) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
-                    if (++cslot == G8_SCALE_STAGES) {
-                        cslot = 0;
-                        c_phase ^= 1u;
-                    }
-                }
-            }
-        }
-        if (warp == 2) cp_async_wait_all();  // no copy is in flight when the CTA leaves
-        __syncwarp();
     } else {
         // ---------------- scaled sums and epilogue (warps 4-11, both CTAs) ----------------
+        if constexpr (MAXN == 256) more_registers<216>();
         constexpr int CHUNKS = MAXN / 32;  // 16-token chunks of this warpgroup's half
         const int q = warp & 3, hw = (warp - 4) >> 2;
         uint8_t* stage_base = epi + (warp - 4) * 4096;
@@ -439,55 +469,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             int g, wb, r0, rows;
             locate(tile, g, wb, r0, rows);
             const int nh = (rows + 31) / 32 * 16;  // tokens of each warpgroup
-            float acc[CHUNKS][2][8];
+            float2 acc[CHUNKS][2][4];
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[c][0][i] = acc[c][1][i] = 0.f;
-            for (int kb = 0; kb < KB; ++kb) {
-                if (lane == 0)
+                for (int i = 0; i < 4; ++i) acc[c][0][i] = acc[c][1][i] = make_float2(0.f, 0.f);
+            // the K blocks, straight through for each number of 32-token batches (the last may reach past this half's tokens:
+            // columns nothing is stored from)
+            const auto mainloop = [&](auto batches) {
+                constexpr int NB = decltype(batches)::value;
+                for (int kb = 0; kb < KB; ++kb) {
                     ok = mbar_wait_within(&sfull_bar[slot], s_phase, abort_flag, limit) &&
                          mbar_wait_within(&tfull_bar[buf], buf_phase, abort_flag, limit);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                tc_fence_after_sync();
-                const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAXN + hw * nh);
-                const float* sc = reinterpret_cast<const float*>(scales + slot * S::SCALE_BYTES) + hw * nh + 2 * (lane & 3);
-                float v[2][2][8];
-                tmem_ld_16x16(t0, v[0][0]);
-                tmem_ld_16x16(t0 + (16u << 16), v[0][1]);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAXN + hw * nh);
+                    const float* sc = reinterpret_cast<const float*>(scales + slot * S::SCALE_BYTES) + hw * nh + 2 * (lane & 3);
+                    float v[2][2][16];
+                    tmem_ld_16x32(t0, v[0][0]);
+                    tmem_ld_16x32(t0 + (16u << 16), v[0][1]);
 #pragma unroll
-                for (int c = 0; c < CHUNKS; ++c) {
-                    if (c * 16 >= nh) break;
-                    tmem_wait_ld(v[c & 1][0], v[c & 1][1]);
-                    if (c + 1 < CHUNKS && (c + 1) * 16 < nh) {
-                        tmem_ld_16x16(t0 + (uint32_t)(16 * (c + 1)), v[(c + 1) & 1][0]);
-                        tmem_ld_16x16(t0 + (uint32_t)(16 * (c + 1)) + (16u << 16), v[(c + 1) & 1][1]);
-                    }
+                    for (int b = 0; b < NB; ++b) {
+                        float2 s0[4], s1[4];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float2 s0 = *reinterpret_cast<const float2*>(sc + 16 * c + 8 * j);
-                        const float2 s1 = GATEUP ? *reinterpret_cast<const float2*>(sc + MAXN + 16 * c + 8 * j) : s0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            acc[c][0][4 * j + i] = fmaf(v[c & 1][0][4 * j + i], (i & 1) ? s0.y : s0.x, acc[c][0][4 * j + i]);
-                            acc[c][1][4 * j + i] = fmaf(v[c & 1][1][4 * j + i], (i & 1) ? s1.y : s1.x, acc[c][1][4 * j + i]);
+                        for (int j = 0; j < 4; ++j) {
+                            s0[j] = *reinterpret_cast<const float2*>(sc + 32 * b + 8 * j);
+                            s1[j] = GATEUP ? *reinterpret_cast<const float2*>(sc + MAXN + 32 * b + 8 * j) : s0[j];
                         }
+                        tmem_wait_ld(v[b & 1][0], v[b & 1][1]);
+                        if (b + 1 < NB) {
+                            tmem_ld_16x32(t0 + (uint32_t)(32 * (b + 1)), v[(b + 1) & 1][0]);
+                            tmem_ld_16x32(t0 + (uint32_t)(32 * (b + 1)) + (16u << 16), v[(b + 1) & 1][1]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int r = 4 * j + 2 * i;
+                                fma2(acc[2 * b + (j >> 1)][0][2 * (j & 1) + i], v[b & 1][0][r], v[b & 1][0][r + 1], s0[j]);
+                                fma2(acc[2 * b + (j >> 1)][1][2 * (j & 1) + i], v[b & 1][1][r], v[b & 1][1][r + 1], s1[j]);
+                            }
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_remote(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
+                        mbar_arrive(&sempty_bar[slot]);
+                    }
+                    if (++buf == NBUF) {
+                        buf = 0;
+                        buf_phase ^= 1u;
+                    }
+                    if (++slot == G8_SCALE_STAGES) {
+                        slot = 0;
+                        s_phase ^= 1u;
                     }
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_remote(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
-                    mbar_arrive(&sempty_bar[slot]);
-                }
-                if (++buf == NBUF) {
-                    buf = 0;
-                    buf_phase ^= 1u;
-                }
-                if (++slot == G8_SCALE_STAGES) {
-                    slot = 0;
-                    s_phase ^= 1u;
+            };
+            if constexpr (MAXN == 64) {
+                mainloop(std::integral_constant<int, 1>());
+            } else {
+                switch ((nh + 31) / 32) {
+                    case 1: mainloop(std::integral_constant<int, 1>()); break;
+                    case 2: mainloop(std::integral_constant<int, 2>()); break;
+                    case 3: mainloop(std::integral_constant<int, 3>()); break;
+                    default: mainloop(std::integral_constant<int, 4>()); break;
                 }
             }
             if (!ok) break;
@@ -507,7 +554,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                     if constexpr (GATEUP) {
                         float h[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) h[i] = swiglu(acc[c][0][i], acc[c][1][i]);
+                        for (int i = 0; i < 4; ++i) {
+                            h[2 * i] = swiglu(acc[c][0][i].x, acc[c][1][i].x);
+                            h[2 * i + 1] = swiglu(acc[c][0][i].y, acc[c][1][i].y);
+                        }
                         // blocks (columns 0-7 | 8-15) of tokens 0-7, then of tokens 8-15
                         const int row = 16 * (c - cc) + (lane & 7) + ((lane >> 4) << 3);
                         const uint32_t at = smem_u32(my_stage) + row * 32 + ((((lane >> 3) & 1) ^ ((row >> 2) & 1)) << 4);
@@ -518,10 +568,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                         for (int j = 0; j < 2; ++j) {  // 8 tokens, 32 columns
                             const int row = 16 * (c - cc) + 8 * j + (lane & 7);
                             const uint32_t at = smem_u32(my_stage) + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4);
-                            stmatrix_x4_trans(at, pack_bf16x2(acc[c][0][4 * j], acc[c][0][4 * j + 1]),
-                                              pack_bf16x2(acc[c][0][4 * j + 2], acc[c][0][4 * j + 3]),
-                                              pack_bf16x2(acc[c][1][4 * j], acc[c][1][4 * j + 1]),
-                                              pack_bf16x2(acc[c][1][4 * j + 2], acc[c][1][4 * j + 3]));
+                            stmatrix_x4_trans(at, pack_bf16x2(acc[c][0][2 * j].x, acc[c][0][2 * j].y),
+                                              pack_bf16x2(acc[c][0][2 * j + 1].x, acc[c][0][2 * j + 1].y),
+                                              pack_bf16x2(acc[c][1][2 * j].x, acc[c][1][2 * j].y),
+                                              pack_bf16x2(acc[c][1][2 * j + 1].x, acc[c][1][2 * j + 1].y));
                         }
                     }
                 }
