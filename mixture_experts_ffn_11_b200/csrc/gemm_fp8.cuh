@@ -346,34 +346,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             __syncwarp();
         } else if (warp == 1) {
             // ---------------- MMA issuer (leader only) ----------------
-            if (leader) {
+            // One lane runs the loop by itself: with the warp brought together after every K block, waiting and issuing took 1250
+            // cycles per K block, more than twice the MMAs' own time.
+            if (leader && lane == 0) {
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, buf_phase = 0;
-                bool ok = true;
-                if (lane == 0) ok = test_stall(never_bar, abort_flag);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+                bool ok = test_stall(never_bar, abort_flag);
                 for (int tile = cluster; tile < total && ok; tile += n_clusters) {
                     int g, wb, r0, rows;
                     locate(tile, g, wb, r0, rows);
                     const uint32_t idesc = idesc_e4m3_f32(256, (rows + 31) / 32 * 32);
                     for (int kb = 0; kb < KB; ++kb) {
-                        if (lane == 0) {
-                            ok = mbar_wait_within(&tempty_bar[buf], buf_phase ^ 1u, abort_flag, limit) &&
-                                 mbar_wait_within(&full_bar[stage], phase, abort_flag, limit);
-                            if (ok) {
-                                tc_fence_after_sync();
-                                const uint32_t sa = smem_u32(stages + stage * S::STAGE_BYTES);
-                                const uint64_t wdesc = smem_desc_sw128(sa), xdesc = smem_desc_sw128(sa + S::W_BYTES);
-                                const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAXN);
-#pragma unroll
-                                for (int k = 0; k < F8_BLOCK / 32; ++k)
-                                    umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
-                                umma_commit_pair_multicast(&empty_bar[stage], 0x3);
-                                umma_commit_pair_multicast(&tfull_bar[buf], 0x3);
-                            }
-                        }
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        ok = mbar_wait_within(&tempty_bar[buf], buf_phase ^ 1u, abort_flag, limit) &&
+                             mbar_wait_within(&full_bar[stage], phase, abort_flag, limit);
                         if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint32_t sa = smem_u32(stages + stage * S::STAGE_BYTES);
+                        const uint64_t wdesc = smem_desc_sw128(sa), xdesc = smem_desc_sw128(sa + S::W_BYTES);
+                        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAXN);
+#pragma unroll
+                        for (int k = 0; k < F8_BLOCK / 32; ++k)
+                            umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
+                        umma_commit_pair_multicast(&tfull_bar[buf], 0x3);
+                        umma_commit_pair_multicast(&empty_bar[stage], 0x3);
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
@@ -384,9 +379,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                         }
                     }
                 }
-                if (lane == 0) umma_commit_pair(final_bar);
-                __syncwarp();
+                umma_commit_pair(final_bar);
             }
+            __syncwarp();
         } else {
             // ---------------- scales (both CTAs) ----------------
             // warp 2: raw scales of each step (tile, K block) into a ring, by asynchronous 4-byte copies (rows start anywhere):
