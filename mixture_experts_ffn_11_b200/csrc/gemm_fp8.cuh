@@ -346,29 +346,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             __syncwarp();
         } else if (warp == 1) {
             // ---------------- MMA issuer (leader only) ----------------
-            // One lane runs the loop by itself: with the warp brought together after every K block, waiting and issuing took 1250
-            // cycles per K block, more than twice the MMAs' own time.
-            if (leader && lane == 0) {
+            // This warp's own time per K block has to stay below the MMAs' (512 cycles at 256 tokens): the whole warp runs the
+            // loop, so that descriptors and addresses stay in uniform registers, and the next K block's barriers are polled
+            // between this one's MMAs and commits.
+            if (leader) {
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, buf_phase = 0;
-                bool ok = test_stall(never_bar, abort_flag);
+                const bool elected = elect_one();
+                bool ok = __all_sync(0xffffffffu, test_stall(never_bar, abort_flag));
+                bool ready = false;  // the coming K block's barriers were seen complete
                 for (int tile = cluster; tile < total && ok; tile += n_clusters) {
                     int g, wb, r0, rows;
                     locate(tile, g, wb, r0, rows);
                     const uint32_t idesc = idesc_e4m3_f32(256, (rows + 31) / 32 * 32);
                     for (int kb = 0; kb < KB; ++kb) {
-                        ok = mbar_wait_within(&tempty_bar[buf], buf_phase ^ 1u, abort_flag, limit) &&
-                             mbar_wait_within(&full_bar[stage], phase, abort_flag, limit);
-                        if (!ok) break;
+                        if (!ready) {
+                            ok = mbar_wait_within(&tempty_bar[buf], buf_phase ^ 1u, abort_flag, limit) &&
+                                 mbar_wait_within(&full_bar[stage], phase, abort_flag, limit);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                        }
                         tc_fence_after_sync();
                         const uint32_t sa = smem_u32(stages + stage * S::STAGE_BYTES);
                         const uint64_t wdesc = smem_desc_sw128(sa), xdesc = smem_desc_sw128(sa + S::W_BYTES);
                         const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAXN);
+                        uint64_t* const tfull = &tfull_bar[buf];
+                        uint64_t* const empty = &empty_bar[stage];
+                        if (elected) {
 #pragma unroll
-                        for (int k = 0; k < F8_BLOCK / 32; ++k)
-                            umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
-                        umma_commit_pair_multicast(&tfull_bar[buf], 0x3);
-                        umma_commit_pair_multicast(&empty_bar[stage], 0x3);
+                            for (int k = 0; k < F8_BLOCK / 32; ++k)
+                                umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
+                        }
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
@@ -377,9 +385,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                             buf = 0;
                             buf_phase ^= 1u;
                         }
+                        const bool te = mbar_test_wait(smem_u32(&tempty_bar[buf]), buf_phase ^ 1u);
+                        const bool fu = mbar_test_wait(smem_u32(&full_bar[stage]), phase);
+                        if (elected) {
+                            umma_commit_pair_multicast(tfull, 0x3);
+                            umma_commit_pair_multicast(empty, 0x3);
+                        }
+                        ready = __all_sync(0xffffffffu, te && fu);
                     }
                 }
-                umma_commit_pair(final_bar);
+                if (elected) umma_commit_pair(final_bar);
             }
             __syncwarp();
         } else {
