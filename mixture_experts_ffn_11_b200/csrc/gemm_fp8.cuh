@@ -11,15 +11,15 @@
 // Roles (384 threads per CTA, both CTAs):
 //   warp 0      TMA producer: per 128-wide K block (one ring stage) this CTA's 128 weight rows (one box) and its half of the
 //               token rows (one box); completion is counted on the leader's full[stage].
-//   warp 1      TMEM allocation; in the leader the MMA issuer: per K block four MMAs (K = 32 each) into the next of NBUF
-//               TMEM buffers, so the tensor cores run ahead of the warps that read them.
+//   warp 1      TMEM allocation; in the leader the MMA issuer: per K block four MMAs (K = 32 each) per token group into its next
+//               TMEM buffer, so the tensor cores run ahead of the warps that read them.
 //   warps 2, 3  scales: sa of the tile's tokens and sw of this CTA's weight rows into a ring by asynchronous copies (warp 2),
 //               their products into another (warp 3). (Loaded through registers two K blocks ahead, the loads' latency set the
 //               pace: 1.2 us per K block at any tile size.)
 //   warps 4-11  two warpgroups, each the four lane quarters of half the tile's tokens: read a K block's sums from TMEM
 //               (tcgen05.ld 16x256b: the layout of an MMA fragment, thread = 2 rows x 2 tokens of each 16 x 8 block),
 //               multiply by the scales, add to the tile's sums in registers (MAXN / 2 per thread); after the last K block
-//               round to bf16, transpose 8 x 8 blocks with stmatrix into [token][column] staging blocks, TMA store.
+//               round to bf16, transpose 8 x 8 blocks with stmatrix into [token][column] staging blocks, 16-byte stores.
 //   gate|up: each quarter of 32 lanes holds 16 gate rows and the 16 up rows of the same columns (one TMA box over the weights
 //   viewed as [G][f/16][2][16][K]), which the 16-lane loads bring into the same thread's registers: SwiGLU needs no exchange.
 // What bounds it: many rows, the tensor cores (at 256 tokens a K block takes 512 cycles of MMA; reading it back takes 256
@@ -52,11 +52,23 @@ struct Gemm8Shape {
     static constexpr int X_BYTES = MAXN / 2 * F8_BLOCK;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
     static constexpr int STAGES = MAXN == 256 ? 5 : 8;
-    static constexpr int NBUF = 512 / MAXN;
+    // A tile of up to 256 tokens is two MMAs per K step, one for each warpgroup's tokens, into two buffers of 128 columns
+    // each: a buffer's way from MMA to free again (commit, read, arrive across the pair) is about 1300 cycles besides the
+    // MMAs, which two 256-column buffers shared by the warpgroups hid less of (prompt products 0.66 ms).
+    static constexpr bool SPLIT = MAXN == 256;
+    static constexpr int GROUPS = SPLIT ? 2 : 1;          // MMAs (token groups) per K step
+    static constexpr int BUF_COLS = MAXN / GROUPS;        // TMEM columns of a buffer
+    static constexpr int NBUF = 512 / MAXN;               // buffers per group
     static constexpr int TILE_W = GATEUP ? 128 : 256;
     static constexpr int SCALE_BYTES = (GATEUP ? 2 : 1) * MAXN * 4;
     static constexpr int RAW_FLOATS = MAXN + 4;
     static constexpr int EPI_BYTES = 8 * 2 * 2048;  // two staging blocks per warp
+    // tokens of the first (or only) MMA and of the second, for `rows` token rows: multiples of 32
+    __device__ static __forceinline__ int group_tokens(int rows, int group) {
+        const int n = (rows + 31) / 32;
+        if (!SPLIT) return 32 * n;
+        return 32 * (group == 0 ? (n + 1) / 2 : n / 2);
+    }
     static constexpr int BAR_BYTES = 512;
     static constexpr int TABLE_BYTES = (2 * (GG_MAX_GROUPS + 1) * 4 + 127) / 128 * 128;
     static constexpr int SMEM_BYTES =
@@ -64,7 +76,7 @@ struct Gemm8Shape {
         G8_RAW_STAGES * RAW_FLOATS * 4 + BAR_BYTES + TABLE_BYTES;
     static_assert(STAGE_BYTES % 1024 == 0, "stage bases stay 1024-byte aligned");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
-    static_assert((2 * STAGES + 2 * NBUF + 2 * G8_SCALE_STAGES + 2 * G8_RAW_STAGES + 2) * 8 + 8 <= BAR_BYTES, "barrier area");
+    static_assert((2 * STAGES + 2 * NBUF * GROUPS + 2 * G8_SCALE_STAGES + 2 * G8_RAW_STAGES + 2) * 8 + 8 <= BAR_BYTES, "barrier area");
 };
 
 // token boxes of 128, 64, 32, 16 rows
@@ -147,35 +159,33 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t a, ui
                  : "memory");
 }
 
-// As flush_staged_block for a block of 32 rows x 16 columns (32 bytes per row, the TMA engine's 32-byte swizzle: the
-// 16-byte unit XORed with row / 4): one TMA store, or stores masked to rows < row_end. All 16 columns are inside.
-__device__ __forceinline__ void flush_staged_block16(uint8_t* stage, int lane, const CUtensorMap* tm_out, __nv_bfloat16* out,
-                                                     int ld, int row0, int row_end, int col0) {
-    if (row0 + 32 <= row_end) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(tm_out, stage, col0, row0);
-            bulk_commit_group();
-        }
-        return;
-    }
+// Send a staged block of 32 rows (row0 .. row0 + 31 of out [M][ld]) x COLS columns from col0: 16-byte stores of the rows
+// < row_end and columns < col_end. The staging rows are COLS * 2 bytes, their 16-byte units XORed so that the 8 rows of
+// an 8 x 8 block fall in different banks. (Plain stores: a TMA store per block made the warps wait for the engine to read the
+// staging buffers, about 1000 cycles per 32 tokens.)
+template <int COLS>
+__device__ __forceinline__ uint32_t staged_unit(int row, int unit) {
+    return (uint32_t)(row * COLS * 2 + ((unit ^ (COLS == 32 ? (row >> 1) & 3 : (row >> 2) & 1)) << 4));
+}
+template <int COLS>
+__device__ __forceinline__ void store_staged_rows(const uint8_t* stage, int lane, __nv_bfloat16* out, int ld, int row0, int row_end,
+                                                  int col0, int col_end) {
+    constexpr int UNITS = COLS / 8, ROWS = 32 / UNITS;  // rows per store instruction
     __syncwarp();
-    const int u = lane & 1;
+    const int u = lane % UNITS;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = i * 16 + (lane >> 1);
-        const uint4 val = *reinterpret_cast<const uint4*>(stage + row * 32 + ((u ^ ((row >> 2) & 1)) << 4));
-        if (row0 + row < row_end) *reinterpret_cast<uint4*>(out + (size_t)(row0 + row) * ld + col0 + u * 8) = val;
+    for (int i = 0; i < UNITS; ++i) {
+        const int row = i * ROWS + lane / UNITS;
+        const uint4 val = *reinterpret_cast<const uint4*>(stage + staged_unit<COLS>(row, u));
+        if (row0 + row < row_end && col0 + u * 8 < col_end)
+            *reinterpret_cast<uint4*>(out + (size_t)(row0 + row) * ld + col0 + u * 8) = val;
     }
-    if (lane == 0) bulk_commit_group();
-    __syncwarp();
 }
 
 template <bool GATEUP, int MAXN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
     grouped_gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Fp8Maps tmX,
-                            const __grid_constant__ CUtensorMap tmO, const Gemm8Args args, int weights_streamed_once) {
+                            const Gemm8Args args, int weights_streamed_once) {
     using S = Gemm8Shape<GATEUP, MAXN>;
     constexpr int STAGES = S::STAGES, NBUF = S::NBUF;
     extern __shared__ uint8_t smem_raw[];
@@ -186,9 +196,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
     float* raw = reinterpret_cast<float*>(scales + G8_SCALE_STAGES * S::SCALE_BYTES);
     uint64_t* full_bar = reinterpret_cast<uint64_t*>(raw + G8_RAW_STAGES * S::RAW_FLOATS);  // used in the leader
     uint64_t* empty_bar = full_bar + STAGES;
-    uint64_t* tfull_bar = empty_bar + STAGES;  // [NBUF]
-    uint64_t* tempty_bar = tfull_bar + NBUF;   // [NBUF], used in the leader
-    uint64_t* sfull_bar = tempty_bar + NBUF;   // [G8_SCALE_STAGES]
+    uint64_t* tfull_bar = empty_bar + STAGES;             // [GROUPS][NBUF]
+    uint64_t* tempty_bar = tfull_bar + S::GROUPS * NBUF;  // [GROUPS][NBUF], used in the leader
+    uint64_t* sfull_bar = tempty_bar + S::GROUPS * NBUF;  // [G8_SCALE_STAGES]
     uint64_t* sempty_bar = sfull_bar + G8_SCALE_STAGES;
     uint64_t* rfull_bar = sempty_bar + G8_SCALE_STAGES;  // [G8_RAW_STAGES]
     uint64_t* rempty_bar = rfull_bar + G8_RAW_STAGES;
@@ -212,9 +222,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
-        for (int b = 0; b < NBUF; ++b) {
+        for (int b = 0; b < S::GROUPS * NBUF; ++b) {
             mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], 16);
+            mbar_init(&tempty_bar[b], 16 / S::GROUPS);  // the warps that read the buffer, of both CTAs
         }
         for (int s = 0; s < G8_SCALE_STAGES; ++s) {
             mbar_init(&sfull_bar[s], 32);
@@ -229,7 +239,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmW);
-        tma_prefetch_desc(&tmO);
 #pragma unroll
         for (int i = 0; i < 4; ++i) tma_prefetch_desc(&tmX.x[i]);
     }
@@ -311,10 +320,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             for (int tile = cluster; tile < total && ok; tile += n_clusters) {
                 int g, wb, r0, rows;
                 locate(tile, g, wb, r0, rows);
-                const int half = (rows + 31) / 32 * 16;  // token rows per CTA (N / 2)
-                const int bi = swap_box_index(half);
-                const int xrow0 = r0 + (int)rank * half;
-                const uint32_t tx = 2u * (uint32_t)(S::W_BYTES + (128 >> bi) * F8_BLOCK);
+                // this CTA's half of each group's tokens, in the smallest box that holds it
+                const int n0 = S::group_tokens(rows, 0), n1 = S::SPLIT ? S::group_tokens(rows, 1) : 0;
+                const int b0 = swap_box_index(n0 / 2), b1 = swap_box_index(n1 / 2);
+                const int x0 = r0 + (int)rank * (n0 / 2), x1 = r0 + n0 + (int)rank * (n1 / 2);
+                const uint32_t tx = 2u * (uint32_t)(S::W_BYTES + ((128 >> b0) + (n1 > 0 ? 128 >> b1 : 0)) * F8_BLOCK);
                 for (int kb = 0; kb < KB; ++kb) {
                     if (lane == 0) {
                         ok = mbar_wait_within(&empty_bar[stage], phase ^ 1u, abort_flag, limit);
@@ -326,7 +336,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                                 tma_load_5d_pair(sw, &tmW, bar, kb * F8_BLOCK, 0, 0, wb * 8 + 4 * (int)rank, g, pol_w);
                             else
                                 tma_load_3d_pair(sw, &tmW, bar, kb * F8_BLOCK, wb * 256 + 128 * (int)rank, g, pol_w);
-                            tma_load_2d_pair(sw + S::W_BYTES, &tmX.x[bi], bar, kb * F8_BLOCK, xrow0, pol_x);
+                            tma_load_2d_pair(sw + S::W_BYTES, &tmX.x[b0], bar, kb * F8_BLOCK, x0, pol_x);
+                            if (S::SPLIT && n1 > 0)
+                                tma_load_2d_pair(sw + S::W_BYTES + S::X_BYTES / 2, &tmX.x[b1], bar, kb * F8_BLOCK, x1, pol_x);
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -350,47 +362,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             // loop, so that descriptors and addresses stay in uniform registers, and the next K block's barriers are polled
             // between this one's MMAs and commits.
             if (leader) {
-                int stage = 0, buf = 0;
-                uint32_t phase = 0, buf_phase = 0;
+                int stage = 0;
+                uint32_t phase = 0;
+                int buf[S::GROUPS] = {};
+                uint32_t buf_phase[S::GROUPS] = {};
                 const bool elected = elect_one();
                 bool ok = __all_sync(0xffffffffu, test_stall(never_bar, abort_flag));
-                bool ready = false;  // the coming K block's barriers were seen complete
+                bool ready = false;  // the stage and the first group's buffer of the coming K block were seen complete
                 for (int tile = cluster; tile < total && ok; tile += n_clusters) {
                     int g, wb, r0, rows;
                     locate(tile, g, wb, r0, rows);
-                    const uint32_t idesc = idesc_e4m3_f32(256, (rows + 31) / 32 * 32);
                     for (int kb = 0; kb < KB; ++kb) {
                         if (!ready) {
-                            ok = mbar_wait_within(&tempty_bar[buf], buf_phase ^ 1u, abort_flag, limit) &&
+                            ok = mbar_wait_within(&tempty_bar[buf[0]], buf_phase[0] ^ 1u, abort_flag, limit) &&
                                  mbar_wait_within(&full_bar[stage], phase, abort_flag, limit);
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
                         }
                         tc_fence_after_sync();
                         const uint32_t sa = smem_u32(stages + stage * S::STAGE_BYTES);
-                        const uint64_t wdesc = smem_desc_sw128(sa), xdesc = smem_desc_sw128(sa + S::W_BYTES);
-                        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAXN);
-                        uint64_t* const tfull = &tfull_bar[buf];
-                        uint64_t* const empty = &empty_bar[stage];
-                        if (elected) {
+                        const uint64_t wdesc = smem_desc_sw128(sa);
 #pragma unroll
-                            for (int k = 0; k < F8_BLOCK / 32; ++k)
-                                umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
+                        for (int gr = 0; gr < S::GROUPS; ++gr) {
+                            const int n = S::group_tokens(rows, gr);
+                            if (n == 0) continue;
+                            uint64_t* const tempty = &tempty_bar[gr * NBUF + buf[gr]];
+                            if (gr > 0 && !__all_sync(0xffffffffu, mbar_test_wait(smem_u32(tempty), buf_phase[gr] ^ 1u))) {
+                                ok = __all_sync(0xffffffffu, mbar_wait_within(tempty, buf_phase[gr] ^ 1u, abort_flag, limit));
+                                if (!ok) break;
+                                tc_fence_after_sync();
+                            }
+                            const uint64_t xdesc = smem_desc_sw128(sa + S::W_BYTES + gr * (S::X_BYTES / 2));
+                            const uint32_t d_tmem = tmem_base + (uint32_t)((gr * NBUF + buf[gr]) * S::BUF_COLS);
+                            const uint32_t idesc = idesc_e4m3_f32(256, n);
+                            if (elected) {
+#pragma unroll
+                                for (int k = 0; k < F8_BLOCK / 32; ++k)
+                                    umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
+                                umma_commit_pair_multicast(&tfull_bar[gr * NBUF + buf[gr]], 0x3);
+                            }
+                            if (++buf[gr] == NBUF) {
+                                buf[gr] = 0;
+                                buf_phase[gr] ^= 1u;
+                            }
                         }
+                        if (!ok) break;
+                        uint64_t* const empty = &empty_bar[stage];
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
-                        if (++buf == NBUF) {
-                            buf = 0;
-                            buf_phase ^= 1u;
-                        }
-                        const bool te = mbar_test_wait(smem_u32(&tempty_bar[buf]), buf_phase ^ 1u);
+                        const bool te = mbar_test_wait(smem_u32(&tempty_bar[buf[0]]), buf_phase[0] ^ 1u);
                         const bool fu = mbar_test_wait(smem_u32(&full_bar[stage]), phase);
-                        if (elected) {
-                            umma_commit_pair_multicast(tfull, 0x3);
-                            umma_commit_pair_multicast(empty, 0x3);
-                        }
+                        if (elected) umma_commit_pair_multicast(empty, 0x3);
                         ready = __all_sync(0xffffffffu, te && fu);
                     }
                 }
@@ -435,22 +459,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                         }
                     }
                 } else {
+                    bool ready = false;
                     for (int kb = 0; kb < KB; ++kb) {
-                        ok = mbar_wait_within(&rfull_bar[slot], phase, abort_flag, limit) &&
-                             mbar_wait_within(&sempty_bar[cslot], c_phase ^ 1u, abort_flag, limit);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
+                        if (!ready) {
+                            ok = mbar_wait_within(&rfull_bar[slot], phase, abort_flag, limit) &&
+                                 mbar_wait_within(&sempty_bar[cslot], c_phase ^ 1u, abort_flag, limit);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                        }
                         const float* from = raw + slot * S::RAW_FLOATS;
                         float* to = reinterpret_cast<float*>(scales + cslot * S::SCALE_BYTES);
-                        const float b0 = from[MAXN], b1 = from[MAXN + 1];
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const float a = from[lane + 32 * i];
-                            to[lane + 32 * i] = a * b0;
-                            if constexpr (GATEUP) to[MAXN + lane + 32 * i] = a * b1;
-                        }
-                        mbar_arrive(&rempty_bar[slot]);
-                        mbar_arrive(&sfull_bar[cslot]);
+                        uint64_t* const r_freed = &rempty_bar[slot];
+                        uint64_t* const filled = &sfull_bar[cslot];
                         if (++slot == G8_RAW_STAGES) {
                             slot = 0;
                             phase ^= 1u;
@@ -459,6 +479,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                             cslot = 0;
                             c_phase ^= 1u;
                         }
+                        const bool next = mbar_test_wait(smem_u32(&rfull_bar[slot]), phase) &
+                                          mbar_test_wait(smem_u32(&sempty_bar[cslot]), c_phase ^ 1u);
+                        const float b0 = from[MAXN], b1 = from[MAXN + 1];
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const float a = from[lane + 32 * i];
+                            to[lane + 32 * i] = a * b0;
+                            if constexpr (GATEUP) to[MAXN + lane + 32 * i] = a * b1;
+                        }
+                        mbar_arrive(r_freed);
+                        mbar_arrive(filled);
+                        ready = kb + 1 < KB && __all_sync(0xffffffffu, next);
                     }
                 }
             }
@@ -470,35 +502,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         if constexpr (MAXN == 256) more_registers<216>();
         constexpr int CHUNKS = MAXN / 32;  // 16-token chunks of this warpgroup's half
         const int q = warp & 3, hw = (warp - 4) >> 2;
+        const int gr = S::SPLIT ? hw : 0;
+        const uint32_t tempty_leader = mapa_shared(smem_u32(tempty_bar), 0);
+        bool ready = false;  // the coming K block's sums and scales were seen complete
         uint8_t* stage_base = epi + (warp - 4) * 4096;
         int buf = 0, slot = 0;
         uint32_t buf_phase = 0, s_phase = 0;
-        uint32_t blocks = 0;
         bool ok = true;
         for (int tile = cluster; tile < total && ok; tile += n_clusters) {
             int g, wb, r0, rows;
             locate(tile, g, wb, r0, rows);
-            const int nh = (rows + 31) / 32 * 16;  // tokens of each warpgroup
+            // this warpgroup's tokens: its own group, or half of the only one (from tile row first, in TMEM column col)
+            const int nh = S::SPLIT ? S::group_tokens(rows, gr) : S::group_tokens(rows, 0) / 2;
+            const int first = S::SPLIT ? hw * S::group_tokens(rows, 0) : hw * nh;
+            const int col = S::SPLIT ? 0 : first;
             float2 acc[CHUNKS][2][4];
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[c][0][i] = acc[c][1][i] = make_float2(0.f, 0.f);
-            // the K blocks, straight through for each number of 32-token batches (the last may reach past this half's tokens:
-            // columns nothing is stored from)
+            // The K blocks, straight through for each number of 32-token batches (the last may reach past this half's tokens:
+            // columns nothing is stored from). A look at a barrier takes some 200 cycles here, also when it is complete, so the
+            // next K block's are looked at behind this one's last loads and the multiply-adds in their shadow.
             const auto mainloop = [&](auto batches) {
                 constexpr int NB = decltype(batches)::value;
                 for (int kb = 0; kb < KB; ++kb) {
-                    ok = mbar_wait_within(&sfull_bar[slot], s_phase, abort_flag, limit) &&
-                         mbar_wait_within(&tfull_bar[buf], buf_phase, abort_flag, limit);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    if (!ready) {
+                        ok = mbar_wait_within(&sfull_bar[slot], s_phase, abort_flag, limit) &&
+                             (NB == 0 || mbar_wait_within(&tfull_bar[gr * NBUF + buf], buf_phase, abort_flag, limit));
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
                     tc_fence_after_sync();
-                    const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAXN + hw * nh);
-                    const float* sc = reinterpret_cast<const float*>(scales + slot * S::SCALE_BYTES) + hw * nh + 2 * (lane & 3);
+                    const uint32_t t0 =
+                        tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((gr * NBUF + buf) * S::BUF_COLS + col);
+                    const float* sc = reinterpret_cast<const float*>(scales + slot * S::SCALE_BYTES) + first + 2 * (lane & 3);
+                    const uint32_t freed = tempty_leader + (uint32_t)((gr * NBUF + buf) * 8);
+                    uint64_t* const s_freed = &sempty_bar[slot];
+                    if (NB > 0 && ++buf == NBUF) {
+                        buf = 0;
+                        buf_phase ^= 1u;
+                    }
+                    if (++slot == G8_SCALE_STAGES) {
+                        slot = 0;
+                        s_phase ^= 1u;
+                    }
+                    bool next = false;
                     float v[2][2][16];
-                    tmem_ld_16x32(t0, v[0][0]);
-                    tmem_ld_16x32(t0 + (16u << 16), v[0][1]);
+                    if constexpr (NB > 0) {
+                        tmem_ld_16x32(t0, v[0][0]);
+                        tmem_ld_16x32(t0 + (16u << 16), v[0][1]);
+                    }
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         float2 s0[4], s1[4];
@@ -511,6 +565,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                         if (b + 1 < NB) {
                             tmem_ld_16x32(t0 + (uint32_t)(32 * (b + 1)), v[(b + 1) & 1][0]);
                             tmem_ld_16x32(t0 + (uint32_t)(32 * (b + 1)) + (16u << 16), v[(b + 1) & 1][1]);
+                        } else {  // everything of this K block is in registers
+                            tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) {
+                                mbar_arrive_remote(freed);
+                                mbar_arrive(s_freed);
+                            }
+                            next = mbar_test_wait(smem_u32(&sfull_bar[slot]), s_phase) &
+                                   mbar_test_wait(smem_u32(&tfull_bar[gr * NBUF + buf]), buf_phase);
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -521,26 +584,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                                 fma2(acc[2 * b + (j >> 1)][1][2 * (j & 1) + i], v[b & 1][1][r], v[b & 1][1][r + 1], s1[j]);
                             }
                     }
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive_remote(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
-                        mbar_arrive(&sempty_bar[slot]);
+                    if constexpr (NB == 0) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_freed);
                     }
-                    if (++buf == NBUF) {
-                        buf = 0;
-                        buf_phase ^= 1u;
-                    }
-                    if (++slot == G8_SCALE_STAGES) {
-                        slot = 0;
-                        s_phase ^= 1u;
-                    }
+                    ready = kb + 1 < KB && __all_sync(0xffffffffu, next);
                 }
             };
             if constexpr (MAXN == 64) {
                 mainloop(std::integral_constant<int, 1>());
             } else {
-                switch ((nh + 31) / 32) {
+                switch (nh / 32) {
+                    case 0: mainloop(std::integral_constant<int, 0>()); break;  // (its only part is to free the scales)
                     case 1: mainloop(std::integral_constant<int, 1>()); break;
                     case 2: mainloop(std::integral_constant<int, 2>()); break;
                     case 3: mainloop(std::integral_constant<int, 3>()); break;
@@ -548,19 +603,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                 }
             }
             if (!ok) break;
-            // this warpgroup's tokens: rows r0 + hw * nh .. row_end
-            const int row_first = r0 + hw * nh, row_end = min(r0 + rows, row_first + nh);
+            const int row_first = r0 + first, row_end = min(r0 + rows, row_first + nh);
             const int col0 = GATEUP ? wb * 128 + 64 * (int)rank + 16 * q : wb * 256 + 128 * (int)rank + 32 * q;
             if (col0 >= args.n_out) continue;
 #pragma unroll
             for (int cc = 0; cc < CHUNKS; cc += 2) {  // blocks of 32 tokens
                 if (row_first + 16 * cc >= row_end) break;
-                uint8_t* my_stage = stage_base + (int)(blocks & 1u) * 2048;
-                ++blocks;
-                if (lane == 0) bulk_wait_group_read<1>();  // the store that last read this buffer is done
-                __syncwarp();
+                uint8_t* my_stage = stage_base + (cc / 2 & 1) * 2048;
 #pragma unroll
-                for (int c = cc; c < (CHUNKS > 1 ? cc + 2 : cc + 1); ++c) {
+                for (int c = cc; c < cc + 2; ++c) {
                     if constexpr (GATEUP) {
                         float h[8];
 #pragma unroll
@@ -570,30 +621,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                         }
                         // blocks (columns 0-7 | 8-15) of tokens 0-7, then of tokens 8-15
                         const int row = 16 * (c - cc) + (lane & 7) + ((lane >> 4) << 3);
-                        const uint32_t at = smem_u32(my_stage) + row * 32 + ((((lane >> 3) & 1) ^ ((row >> 2) & 1)) << 4);
-                        stmatrix_x4_trans(at, pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]), pack_bf16x2(h[4], h[5]),
-                                          pack_bf16x2(h[6], h[7]));
+                        stmatrix_x4_trans(smem_u32(my_stage) + staged_unit<16>(row, (lane >> 3) & 1), pack_bf16x2(h[0], h[1]),
+                                          pack_bf16x2(h[2], h[3]), pack_bf16x2(h[4], h[5]), pack_bf16x2(h[6], h[7]));
                     } else {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {  // 8 tokens, 32 columns
                             const int row = 16 * (c - cc) + 8 * j + (lane & 7);
-                            const uint32_t at = smem_u32(my_stage) + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4);
-                            stmatrix_x4_trans(at, pack_bf16x2(acc[c][0][2 * j].x, acc[c][0][2 * j].y),
+                            stmatrix_x4_trans(smem_u32(my_stage) + staged_unit<32>(row, lane >> 3),
+                                              pack_bf16x2(acc[c][0][2 * j].x, acc[c][0][2 * j].y),
                                               pack_bf16x2(acc[c][0][2 * j + 1].x, acc[c][0][2 * j + 1].y),
                                               pack_bf16x2(acc[c][1][2 * j].x, acc[c][1][2 * j].y),
                                               pack_bf16x2(acc[c][1][2 * j + 1].x, acc[c][1][2 * j + 1].y));
                         }
                     }
                 }
-                if constexpr (GATEUP)
-                    flush_staged_block16(my_stage, lane, &tmO, args.out, args.n_out, row_first + 16 * cc, row_end, col0);
-                else
-                    flush_staged_block(my_stage, lane, &tmO, args.out, args.n_out, row_first + 16 * cc, row_end, col0,
-                                       args.n_out);
+                store_staged_rows<GATEUP ? 16 : 32>(my_stage, lane, args.out, args.n_out, row_first + 16 * cc, row_end, col0,
+                                                    args.n_out);
             }
         }
-        if (lane == 0) bulk_wait_all();  // the output stores have landed before the CTA leaves
-        __syncwarp();
     }
 
     tc_fence_before_sync();

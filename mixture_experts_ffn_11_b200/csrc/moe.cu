@@ -796,7 +796,7 @@ template <bool GATEUP, int MAXN>
 moe_status_t launch_fp8(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, const int32_t* offsets, int G, int M,
                         int d, int f, moe_bf16_t* out, int sms, cudaStream_t stream) {
     using S = Gemm8Shape<GATEUP, MAXN>;
-    CUtensorMap tw, to;
+    CUtensorMap tw;
     Fp8Maps tx;
     const int K = GATEUP ? d : f, n_out = GATEUP ? f : d;
     const cuuint64_t k = (cuuint64_t)K, n = (cuuint64_t)n_out, g = (cuuint64_t)G;
@@ -819,13 +819,6 @@ moe_status_t launch_fp8(const uint8_t* a, const float* sa, const uint8_t* w, con
         const cuuint32_t box[2] = {F8_BLOCK, (cuuint32_t)(128 >> i)};
         st = make_tmap(&tx.x[i], a, 2, xdims, xstr, box, u8);
     }
-    if (st == MOE_OK) {  // 32 tokens x the columns of one warp
-        const cuuint64_t dims[2] = {n, (cuuint64_t)M};
-        const cuuint64_t str[1] = {n * 2};
-        const cuuint32_t box[2] = {GATEUP ? 16 : 32, 32};
-        st = make_tmap(&to, out, 2, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                       GATEUP ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B);
-    }
     if (st != MOE_OK) return st;
     Gemm8Args args;
     args.group_offsets = offsets;
@@ -841,7 +834,7 @@ moe_status_t launch_fp8(const uint8_t* a, const float* sa, const uint8_t* w, con
     const int clusters = (int)(upper < sms / 2 ? upper : sms / 2);
     const int streamed_once = (long)M <= (long)G * MAXN ? 1 : 0;
     const cudaError_t e = launch_pdl(grouped_gemm_fp8_kernel<GATEUP, MAXN>, dim3(2 * clusters), dim3(G8_THREADS), S::SMEM_BYTES,
-                                     stream, tw, tx, to, args, streamed_once);
+                                     stream, tw, tx, args, streamed_once);
     return check_launch(GATEUP ? "grouped_gemm_gateup_fp8" : "grouped_gemm_down_fp8", e);
 }
 
