@@ -391,6 +391,36 @@ moe_status_t moe_unpermute_combine(const moe_bf16_t* y_perm, const int32_t* inv_
                                    const moe_bf16_t* shared, int T, int d, int k, moe_bf16_t* y,
                                    cudaStream_t stream);
 
+/* ---- The whole layer for few tokens ----
+ * One call for a layer of T <= MOE_FEW_TOKENS_MAX tokens with bf16 weights (a
+ * decoding step of a few streams), in two kernels instead of eight: router,
+ * top-k, gate|up, SwiGLU, down, weighted sum (+ shared expert). Same formulas
+ * as the separate calls; the routing weight is applied to the fp32 SwiGLU value
+ * before its rounding to bf16 (the down projection is linear), and a token's
+ * experts are summed in fp32 without rounding in between:
+ *   h_tj = bf16(w_tj * silu(x_t Wg_e^T) * (x_t Wu_e^T)), e = topk_idx[t][j]
+ *   y_t  = bf16(sum_j Wd_e h_tj + Wd_shared bf16(silu(x_t Wg_s^T) * (x_t Wu_s^T)))
+ * Every sum runs in an order fixed by the sizes and the routing: the same
+ * inputs give the same bits. A token with NaN in it gives NaN in its own row
+ * (its NaN logits count as the lowest, so its expert ids stay in range).
+ *   x [T][d] bf16, w_router [E][d] fp32, bias [E] fp32 or NULL,
+ *   w_gateup [E][2f][d], w_down [E][d][f] bf16 (as in the grouped GEMMs),
+ *   w_gateup_shared [2fs][d], w_down_shared [d][fs] bf16, or NULL with fs = 0
+ *   logits_out [T][E] fp32, topk_idx [T][k] int32, topk_w [T][k] fp32, y [T][d] bf16: written
+ *   ws  moe_few_tokens_workspace_size(T, d, f, fs, E, k) bytes, 256-byte
+ *       aligned, need not be initialised; calls that can overlap on the GPU
+ *       each need one of their own
+ * The second kernel is a cooperative launch (its CTAs meet at a barrier): it
+ * starts once every SM has room for it. Limits: those of moe_route_topk; f
+ * and fs multiples of 8; d * f below 2^31, d * fs below 2^30. */
+#define MOE_FEW_TOKENS_MAX 32
+size_t moe_few_tokens_workspace_size(int T, int d, int f, int fs, int E, int k);
+moe_status_t moe_few_tokens(const moe_bf16_t* x, const float* w_router, const float* bias, const moe_bf16_t* w_gateup,
+                            const moe_bf16_t* w_down, const moe_bf16_t* w_gateup_shared,
+                            const moe_bf16_t* w_down_shared, int T, int d, int f, int fs, int E, int k,
+                            moe_route_mode_t mode, float* logits_out, int32_t* topk_idx, float* topk_w, moe_bf16_t* y,
+                            void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ---- Backward pass (training) ----
  * The blog post trains MoE layers through the same grouped expert backend
  * ("Training MoEs with Transformers"). With the top-k selection held fixed (it

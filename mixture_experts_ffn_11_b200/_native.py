@@ -27,7 +27,8 @@ EXPORTS = ("moe_route_topk", "moe_router_split_weights", "moe_route_topk_split",
            "moe_grouped_gemm_gateup", "moe_grouped_gemm_gateup_gather_workspace_size",
            "moe_grouped_gemm_gateup_gather", "moe_gather_rows", "moe_grouped_gemm_down",
            "moe_grouped_gemm_down_combine_workspace_size", "moe_grouped_gemm_down_combine", "moe_mxfp4_quantize", "moe_grouped_gemm_gateup_mxfp4",
-           "moe_grouped_gemm_down_mxfp4", "moe_fp8_block_quantize", "moe_fp8_row_quantize",
+           "moe_grouped_gemm_down_mxfp4", "moe_few_tokens_workspace_size", "moe_few_tokens",
+           "moe_fp8_block_quantize", "moe_fp8_row_quantize",
            "moe_grouped_gemm_gateup_fp8", "moe_grouped_gemm_down_fp8", "moe_unpermute_combine", "moe_grouped_gemm_gateup_preact",
            "moe_grouped_gemm_gateup_save",
            "moe_swiglu_backward", "moe_permute_backward", "moe_transpose_weights",
@@ -68,6 +69,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_mxfp4_quantize": [vp, ci, ci, ci, vp, vp, vp],
         "moe_grouped_gemm_gateup_mxfp4": [vp, vp, vp, vp, ci, ci, ci, ci, vp, vp],
         "moe_grouped_gemm_down_mxfp4": [vp, vp, vp, vp, ci, ci, ci, ci, vp, vp],
+        "moe_few_tokens_workspace_size": [ci, ci, ci, ci, ci, ci],
+        "moe_few_tokens": [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, ci, vp, vp, vp, vp, vp, sz, vp],
         "moe_fp8_block_quantize": [vp, ci, ci, ci, vp, vp, vp],
         "moe_fp8_row_quantize": [vp, vp, ci, ci, ci, vp, vp, vp],
         "moe_grouped_gemm_gateup_fp8": [vp, vp, vp, vp, vp, ci, ci, ci, ci, vp, vp],
@@ -103,6 +106,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_grouped_gemm_down_combine_workspace_size.restype = sz
     lib.moe_router_backward_workspace_size.restype = sz
     lib.moe_block_norm_backward_workspace_size.restype = sz
+    lib.moe_few_tokens_workspace_size.restype = sz
     lib.moe_last_error_string.restype = ctypes.c_char_p
     return lib
 
@@ -507,6 +511,38 @@ def _ws(t, dev):
     if t is None:
         return None, 0
     return _want(t, torch.uint8, t.shape, "ws", dev), t.numel()
+
+
+# ---- the whole layer for few tokens ----
+
+FEW_TOKENS_MAX = 32  # MOE_FEW_TOKENS_MAX in include/moe.h
+
+
+def few_tokens_workspace_size(T: int, d: int, f: int, fs: int, E: int, k: int) -> int:
+    """Bytes of workspace few_tokens needs for T tokens; fs = 0 without a shared expert."""
+    return int(_lib.moe_few_tokens_workspace_size(T, d, f, fs, E, k))
+
+
+def few_tokens(x, w_router, bias, w_gateup, w_down, w_gateup_shared, w_down_shared, k, mode, logits, topk_idx, topk_w, y, ws,
+               stream=None):
+    """The whole layer for T <= 32 tokens x [T, d]: logits [T, E], topk_idx and topk_w [T, k], y [T, d]. Weights as MoEFFN's
+    (bf16); shared ones and bias may be None."""
+    dev = _device_of(x, "x")
+    T, d = x.shape
+    E, f = w_down.shape[0], w_down.shape[2]
+    if mode not in ROUTE_MODES:
+        raise ValueError(f"unknown routing mode {mode!r}")
+    if (w_gateup_shared is None) != (w_down_shared is None):
+        raise ValueError("a shared expert has both its weights, or none")
+    fs = 0 if w_down_shared is None else w_down_shared.shape[1]
+    bf, f32 = torch.bfloat16, torch.float32
+    _run("moe_few_tokens", _lib.moe_few_tokens, dev, stream, _want(x, bf, (T, d), "x", dev),
+         _want(w_router, f32, (E, d), "w_router", dev), None if bias is None else _want(bias, f32, (E,), "bias", dev),
+         _want(w_gateup, bf, (E, 2 * f, d), "w_gateup", dev), _want(w_down, bf, (E, d, f), "w_down", dev),
+         None if fs == 0 else _want(w_gateup_shared, bf, (2 * fs, d), "w_gateup_shared", dev),
+         None if fs == 0 else _want(w_down_shared, bf, (d, fs), "w_down_shared", dev), T, d, f, fs, E, k, ROUTE_MODES[mode],
+         _want(logits, f32, (T, E), "logits", dev), _want(topk_idx, torch.int32, (T, k), "topk_idx", dev),
+         _want(topk_w, f32, (T, k), "topk_w", dev), _want(y, bf, (T, d), "y", dev), *_ws(ws, dev))
 
 
 # ---- e4m3 values with a scale per block of 128 ----

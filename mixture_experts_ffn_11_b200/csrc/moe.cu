@@ -27,6 +27,7 @@
 #include "gemm_wgrad.cuh"
 #include "backward.cuh"
 #include "combine.cuh"
+#include "few_tokens.cuh"
 #include "block_norm.cuh"
 
 using namespace moe;
@@ -197,6 +198,8 @@ cudaError_t set_router_attributes() {
     return e;
 }
 
+cudaError_t set_few_attributes();
+
 struct DeviceInfo {
     bool ready = false;
     bool sm100 = false;
@@ -224,6 +227,7 @@ moe_status_t device_info(DeviceInfo& out) {
         if (di.sm100) {
             e = set_gemm_attributes();
             if (e == cudaSuccess) e = set_router_attributes();
+            if (e == cudaSuccess) e = set_few_attributes();
             if (e != cudaSuccess)
                 return fail(MOE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         }
@@ -785,6 +789,54 @@ moe_status_t route_impl(const moe_bf16_t* x, const float* w_router, const moe_bf
     const cudaError_t e = launch_pdl(topk_kernel, dim3((T + TOPK_WARPS - 1) / TOPK_WARPS), dim3(TOPK_WARPS * 32), 0,
                                      stream, logits_out, T, E, k, (int)mode, topk_idx, topk_w);
     return check_launch("topk", e);
+}
+
+}  // namespace
+
+// ---- the whole layer for few tokens ----
+namespace {
+
+struct FewWorkspace {  // byte offsets: counters | h | parts
+    size_t h, part, bytes;
+    int n_counters, ldh;
+};
+FewWorkspace few_workspace(int T, int d, int f, int fs, int k) {
+    FewWorkspace w;
+    w.n_counters = 1 + (d + 15) / 16;
+    w.ldh = f > fs ? f : fs;
+    w.h = ((size_t)w.n_counters * 4 + 255) / 256 * 256;
+    w.part = w.h + ((size_t)(T * k + (fs ? T : 0)) * w.ldh * 2 + 255) / 256 * 256;
+    w.bytes = w.part + (size_t)FT_MAX_CTAS * 2 * 16 * (T <= 8 ? 8 : (T <= 16 ? 16 : 32)) * 4;
+    return w;
+}
+
+template <int NT>
+size_t few_smem(int slots, int E) {
+    return (size_t)2 * FT_WARPS * NT * 32 * 16 + (size_t)FewTables::words(slots, E) * 4 + (size_t)(slots + 1) * 8 * NT * 2;
+}
+
+cudaError_t set_few_attributes() {
+    const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(few_tokens_kernel<1>, a, (int)few_smem<1>(8 * 32, 1024));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(few_tokens_kernel<2>, a, (int)few_smem<2>(16 * 32, 1024));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(few_tokens_kernel<4>, a, (int)few_smem<4>(FT_MAX_T * 32, 1024));
+    return e;
+}
+
+// One CTA per SM, all of them resident at once (they meet at a barrier): a cooperative launch.
+template <int NT>
+cudaError_t launch_few(const FewArgs& a, int grid, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(FT_THREADS);
+    cfg.dynamicSmemBytes = few_smem<NT>(a.T * a.k, a.E);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, few_tokens_kernel<NT>, a);
 }
 
 }  // namespace
@@ -1507,6 +1559,66 @@ moe_status_t moe_router_backward(const moe_bf16_t* x, const float* w_router, con
                    (const float*)dl_tk, w_router, reinterpret_cast<const __nv_bfloat16*>(dx_addend), T, d, E, k,
                    reinterpret_cast<__nv_bfloat16*>(dx));
     return check_launch("router_input_grad", e);
+}
+
+// ---- the whole layer for few tokens ----
+
+size_t moe_few_tokens_workspace_size(int T, int d, int f, int fs, int E, int k) {
+    if (T < 1 || T > MOE_FEW_TOKENS_MAX || d < 8 || f < 8 || fs < 0 || E < 1 || k < 1 || k > 32) return 0;
+    return (few_workspace(T, d, f, fs, k).bytes + 255) / 256 * 256;
+}
+
+moe_status_t moe_few_tokens(const moe_bf16_t* x, const float* w_router, const float* bias, const moe_bf16_t* w_gateup,
+                            const moe_bf16_t* w_down, const moe_bf16_t* w_gateup_shared, const moe_bf16_t* w_down_shared, int T,
+                            int d, int f, int fs, int E, int k, moe_route_mode_t mode, float* logits_out, int32_t* topk_idx,
+                            float* topk_w, moe_bf16_t* y, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    moe_status_t st = check_route_sizes(T, E, k);
+    if (st != MOE_OK) return st;
+    if (mode < MOE_ROUTE_TOPK_SOFTMAX || mode > MOE_ROUTE_SIGMOID_TOPK_NORM)
+        return fail(MOE_ERR_INVALID_ARG, "unknown routing mode %d", (int)mode);
+    if (T > MOE_FEW_TOKENS_MAX) return fail(MOE_ERR_INVALID_ARG, "T=%d above %d", T, MOE_FEW_TOKENS_MAX);
+    if (d < 8 || f < 8 || d % 8 || f % 8 || fs < 0 || fs % 8)
+        return fail(MOE_ERR_INVALID_ARG, "d=%d and f=%d must be positive multiples of 8, fs=%d 0 or one", d, f, fs);
+    if ((long)d * f > 0x7fffffffL || (long)d * fs > 0x3fffffffL) return fail(MOE_ERR_INVALID_ARG, "d * f too large");
+    if (T == 0) return MOE_OK;
+    if (!x || !w_router || !w_gateup || !w_down || !logits_out || !topk_idx || !topk_w || !y ||
+        (fs > 0 && (!w_gateup_shared || !w_down_shared)))
+        return fail(MOE_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gateup) || !aligned16(w_down) || !aligned16(w_gateup_shared) ||
+        !aligned16(w_down_shared) || !aligned16(y))
+        return fail(MOE_ERR_INVALID_ARG, "x, y and weight pointers must be 16-byte aligned");
+    const FewWorkspace w = few_workspace(T, d, f, fs, k);
+    if (!ws || ws_bytes < w.bytes)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", w.bytes, ws ? ws_bytes : (size_t)0);
+    if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(MOE_ERR_WORKSPACE, "workspace not 256-byte aligned");
+    DeviceInfo di;
+    if ((st = device_info(di)) != MOE_OK) return st;
+    uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+    FewArgs a{};
+    a.x = reinterpret_cast<const __nv_bfloat16*>(x);
+    a.w_gateup = reinterpret_cast<const __nv_bfloat16*>(w_gateup);
+    a.w_down = reinterpret_cast<const __nv_bfloat16*>(w_down);
+    a.s_gateup = reinterpret_cast<const __nv_bfloat16*>(w_gateup_shared);
+    a.s_down = reinterpret_cast<const __nv_bfloat16*>(w_down_shared);
+    a.logits = logits_out, a.topk_idx = topk_idx, a.topk_w = topk_w;
+    a.y = reinterpret_cast<__nv_bfloat16*>(y);
+    a.counters = reinterpret_cast<int*>(base);
+    a.h = reinterpret_cast<__nv_bfloat16*>(base + w.h);
+    a.part = reinterpret_cast<float*>(base + w.part);
+    a.T = T, a.d = d, a.f = f, a.fs = fs, a.E = E, a.k = k, a.mode = (int)mode, a.ldh = w.ldh;
+    cudaError_t e = launch_pdl(few_tokens_logits_kernel, dim3(E), dim3(FT_LOGIT_THREADS), 0, stream, a.x, w_router, bias, T, d, E,
+                               logits_out, a.counters, w.n_counters);
+    if ((st = check_launch("few_tokens (logits)", e)) != MOE_OK) return st;
+    // at least one step of the down projection per CTA (some expert is always active)
+    const long steps = (long)((f + FT_KC - 1) / FT_KC) * ((d + 15) / 16);
+    const int grid = (int)std::min<long>(steps, std::min(di.sms, FT_MAX_CTAS));
+    if (T <= 8)
+        e = launch_few<1>(a, grid, stream);
+    else if (T <= 16)
+        e = launch_few<2>(a, grid, stream);
+    else
+        e = launch_few<4>(a, grid, stream);
+    return check_launch("few_tokens", e);
 }
 
 // ---- e4m3 operands with a scale per block of 128 ----

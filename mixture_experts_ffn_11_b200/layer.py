@@ -47,10 +47,14 @@ class MoEFFN:
     pass then gathers x_perm itself. Off by default: on B200 the separate gather and combine kernels are faster
     (the per-row gather loads and the combine's arrival counting slow the GEMMs by more than the two kernels
     take).
+    few: with bf16 weights and 1 to 32 tokens, run the whole layer in two kernels (moe_few_tokens) instead of eight. Results
+    agree to rounding, not bit for bit (the routing weight is applied before h is rounded, and the experts' outputs are
+    summed without rounding). Not used by a training forward, whose backward pass reads the separate calls' buffers.
     """
 
     def __init__(self, w_router, w_gateup, w_down, k: int, route: str = "topk_softmax", bias=None,
-                 w_gateup_shared=None, w_down_shared=None, weights: str = "bf16", fused: bool = False):
+                 w_gateup_shared=None, w_down_shared=None, weights: str = "bf16", fused: bool = False,
+                 few: bool = False):
         self.E, self.d = w_router.shape
         self.f = w_gateup.shape[1] // 2
         self.k = k
@@ -61,6 +65,7 @@ class MoEFFN:
             raise ValueError(f"unknown weight format {weights!r}")
         self.weights = weights
         self.fused = fused
+        self.few = few
         self._x_perm_valid = False
         self.w_router, self.w_gateup, self.w_down, self.bias = w_router, w_gateup, w_down, bias
         self.w_gateup_shared, self.w_down_shared = w_gateup_shared, w_down_shared
@@ -162,7 +167,7 @@ class MoEFFN:
         timing: optional dict; if given, a (start, end) pair of CUDA events is recorded around each stage
         ("route", "permute", "gateup", "down", "combine" on the layer's stream; "shared", the always-on
         expert, on the side stream where it overlaps routing and grouping: its GEMMs, or, folded into the routed
-        GEMMs (MXFP4), the copy of its rows).
+        GEMMs (MXFP4), the copy of its rows; "few" alone, the whole layer, where the few-token kernels run).
         """
         T = x.shape[0]
         b = self.buffers(T)
@@ -176,6 +181,16 @@ class MoEFFN:
                 timing[name] = (torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
             timing[name][0 if first else 1].record(s)
 
+        if self._few(T) and not train:
+            if "few_ws" not in b:
+                n = N.few_tokens_workspace_size(T, self.d, self.f, self.shared_f, self.E, self.k)
+                b["few_ws"] = torch.empty(n, dtype=torch.uint8, device=self.device)
+            mark("few", True)
+            N.few_tokens(x, self.w_router, self.bias, self.w_gateup, self.w_down, self.w_gateup_shared, self.w_down_shared,
+                         self.k, self.route, b["logits"], b["topk_idx"], b["topk_w"], b["y"], b["few_ws"], s)
+            mark("few", False)
+            self._x = None  # nothing is kept for a backward pass
+            return b["y"]
         shared = None
         if self.shared_f:
             side = self._side
@@ -247,6 +262,10 @@ class MoEFFN:
         T tokens."""
         return (self.fused and self.weights == "bf16" and T > 0
                 and N.grouped_gemm_gateup_gather_workspace_size(self.E, T * self.k, self.d) == 0)
+
+    def _few(self, T: int) -> bool:
+        """Whether forward() runs the whole layer in the few-token kernels for T tokens."""
+        return self.few and self.weights == "bf16" and 0 < T <= N.FEW_TOKENS_MAX
 
     def _fold(self, T: int) -> bool:
         """Whether forward() computes the shared expert inside the routed MXFP4 GEMMs for T tokens: when the
@@ -446,9 +465,11 @@ class MoEFFN:
         tensor-core path with fused top-k is taken (E <= 128, T >= 2048), else logits + top-k;
         permute 4, gate|up, down, combine 1 each (fused: permute 3, gate|up 1, down with combine 1; train: the
         gate|up that keeps its pre-activations is 1 kernel with 128 rows or more per expert, else 2); the shared
-        expert 2 more (1 folded: the copy of its rows)."""
+        expert 2 more (1 folded: the copy of its rows). few: 2 in all where it is taken."""
         if T <= 0:
             return 0
+        if self._few(T) and not train:
+            return 2
         route = 1 if (self.E <= 128 and T >= 2048) else 2
         if train and self.weights == "bf16":
             body = 4 + 3 + (0 if T * self.k >= 128 * self.E else 1)
