@@ -11,17 +11,20 @@
 // few_tokens_kernel is one cooperative launch of one CTA per SM:
 //   route    every CTA picks the top-k of all tokens itself, from the logits (a warp per token), and lists the active experts
 //            and their tokens in shared memory.
-//   gate|up  unit = (active expert, 8 columns of h): 8 gate and 8 up rows as the 16 rows of mma.m16n8k16, the expert's tokens
-//            as its 8 columns (as many MMAs as it takes), K split over the CTA's 16 warps, summed through shared memory. A
-//            thread's accumulators hold the gate and the up value of the same column: SwiGLU, then h to the workspace.
-//   barrier  over the grid, a counter in the workspace (bounded wait). Each warp's first loads of W_down go out before it.
-//   down     the (16 output columns) x (active expert, K) steps, laid end to end, are cut into equal ranges, one per CTA: no
+//   gate|up  unit = (active expert, 16 columns of h): 2 x (8 gate and 8 up rows) as the 16 rows of mma.m16n8k16, the expert's
+//            tokens as its 8 columns (as many MMAs as it takes), K dealt out to the CTA's 16 warps in steps of 32, their sums
+//            added through shared memory. A thread's accumulators hold the gate and the up value of the same column: SwiGLU,
+//            then h to the workspace.
+//   barrier  over the grid, a counter in the workspace (bounded wait). The first loads of W_down go out before it.
+//   down     the (32 output columns) x (active expert, K) steps, laid end to end, are cut into equal ranges, one per CTA: no
 //            tail, whatever the routing. A block of columns cut between CTAs is finished by the last of them to arrive, which
 //            adds their sums in the CTAs' order: no waiting, the same bits every time.
 // Loads: a thread's 16 bytes of a weight row are 8 consecutive k; the 4 threads of a row cover 64 bytes. Which k an MMA's
 // column stands for does not matter as long as both operands agree, so those 8 values are used as they come, two MMAs' worth,
-// against the same 8 of the token's row: no shuffles, no shared memory for weights. Two batches of 4 such loads x 2 rows per
-// thread are in flight (up to 128 KB per SM).
+// against the same 8 of the token's row: no shuffles. Each thread copies its own operands of the coming steps into its own
+// shared memory (cp.async, a ring of STAGES steps) and reads them back itself: no barrier, and the ring runs on across the
+// units' ends, with up to 128 KB per SM in flight. (Held in registers, in batches of 4 steps, the loads stopped at every
+// batch and unit: 66 us instead of the figure below for one token.)
 #pragma once
 #include "common.cuh"
 #include "gemm.cuh"
@@ -34,7 +37,10 @@ constexpr int FT_WARPS = 16;
 constexpr int FT_THREADS = FT_WARPS * 32;
 constexpr int FT_MAX_CTAS = 148;
 constexpr int FT_KC = 32;     // k values of a step: 64 bytes of a weight row
-constexpr int FT_BATCH = 4;   // steps a warp loads together
+template <int NT>
+constexpr int FT_STAGES = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // ring of steps, (4 + NT) x 8 KB each
+template <int NT>
+constexpr int FT_RED_BLOCKS = NT == 4 ? 1 : 2;  // 16-row blocks whose sums the reduction buffer holds at a time, NT x 8 KB each
 constexpr int FT_LOGIT_THREADS = 256;
 
 // ---- logits: one CTA per expert, fp32, 8 tokens at a time; also clears the counters of the kernel behind it ----
@@ -92,17 +98,19 @@ struct FewArgs {
     float* topk_w;                  // [T][k]
     __nv_bfloat16* y;               // [T][d]
     __nv_bfloat16* h;               // workspace [T*k + T][ldh]: row t*k+j, or T*k + t for the shared expert
-    float* part;                    // workspace [CTAs][2][16 * 8NT]
-    int* counters;                  // workspace [1 + ceil(d/16)], zero
+    float* part;                    // workspace [CTAs][2][32 * 8NT]
+    int* counters;                  // workspace [1 + ceil(d/32)], zero
     int T, d, f, fs, E, k, mode, ldh;
 };
 
 // Shared memory of few_tokens_kernel besides its reduction buffers, in 4-byte words: slots = T * k.
 struct FewTables {
-    // idx [slots], w [slots], rank [slots], count [E], place [E] (position among the active experts), active [slots + 1],
-    // first [slots + 2] (prefix of the active experts' counts), rows [slots] (slots by active expert), then slot_of as 16-bit:
-    // [slots + 1][8NT] slot of (active expert, token) or -1
-    static __host__ __device__ int words(int slots, int E) { return 3 * slots + 2 * E + (slots + 1) + (slots + 2) + slots + 2; }
+    // idx [slots], w [slots], count [E], place [E] (position among the active experts), active [slots + 1],
+    // first [slots + 2] (prefix of the active experts' counts), rows [slots] (slots by active expert), 2 flags, tiles
+    // [slots + 1], then as 8-bit [slots + 1][8NT]: which of its k choices the token has the active expert as, or -1
+    static __host__ __device__ int words(int slots, int E) {
+        return 2 * slots + 2 * E + (slots + 1) + (slots + 2) + slots + 2 + (slots + 1);
+    }
 };
 
 // D (16 x 8, fp32) += A (16 x 16, bf16) B (16 x 8, bf16)
@@ -113,12 +121,18 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Weights are read once: not kept in L1.
-__device__ __forceinline__ uint4 ld_weight(const __nv_bfloat16* p) {
+// Asynchronous copy of 16 bytes to this thread's place in shared memory (zeros where `inside` is false: nothing is read).
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool inside) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(inside ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
@@ -149,20 +163,23 @@ __device__ __forceinline__ bool grid_barrier(int* counter, int* s_flag) {
 template <int NT>
 __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr int RED = FT_WARPS * NT * 32;                     // float4 per reduction buffer
-    float4* red = reinterpret_cast<float4*>(smem_raw);          // [2][warp][NT][lane]
-    int* words = reinterpret_cast<int*>(red + 2 * RED);
+    constexpr int STAGES = FT_STAGES<NT>, SLOT_BYTES = FT_THREADS * 16, STAGE_BYTES = (4 + NT) * SLOT_BYTES;
+    const uint32_t ring = smem_u32(smem_raw) + threadIdx.x * 16;  // this thread's 16 bytes of slot 0, stage 0
+    float4* red = reinterpret_cast<float4*>(smem_raw + STAGES * STAGE_BYTES);  // [warp][RB][NT][lane]
+    constexpr int RB = FT_RED_BLOCKS<NT>;
+    int* words = reinterpret_cast<int*>(red + FT_WARPS * RB * NT * 32);
     const int slots = p.T * p.k;
     int* s_idx = words;
     float* s_w = reinterpret_cast<float*>(s_idx + slots);
-    int* s_rank = s_idx + 2 * slots;
-    int* s_count = s_rank + slots;
+    int* s_rank = reinterpret_cast<int*>(red);  // [slots] until the first sums
+    int* s_count = s_idx + 2 * slots;
     int* s_place = s_count + p.E;
     int* s_active = s_place + p.E;
     int* s_first = s_active + slots + 1;
     int* s_rows = s_first + slots + 2;
     int* s_n = s_rows + slots;  // number of active experts; flag of the barrier and of the last arrival
-    int16_t* s_slot = reinterpret_cast<int16_t*>(words + FewTables::words(slots, p.E));
+    int* s_tiles = s_n + 2;       // [slots + 1] bit n: the active expert has a token among tokens 8n .. 8n + 7
+    int8_t* s_choice = reinterpret_cast<int8_t*>(words + FewTables::words(slots, p.E));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
     const int T = p.T;
@@ -178,7 +195,8 @@ __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs
         warp_route_select(logit, p.E, p.k, p.mode, s_idx + t * p.k, s_w + t * p.k);
     }
     for (int e = threadIdx.x; e < p.E; e += FT_THREADS) s_count[e] = 0;
-    for (int i = threadIdx.x; i < (slots + 1) * 8 * NT; i += FT_THREADS) s_slot[i] = -1;
+    for (int i = threadIdx.x; i < (slots + 1) * 8 * NT; i += FT_THREADS) s_choice[i] = -1;
+    for (int i = threadIdx.x; i <= slots; i += FT_THREADS) s_tiles[i] = 0;
     __syncthreads();
     for (int s = threadIdx.x; s < slots; s += FT_THREADS) {
         const int e = s_idx[s];
@@ -222,247 +240,297 @@ __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs
     for (int s = threadIdx.x; s < slots; s += FT_THREADS) {
         const int at = s_place[s_idx[s]];
         s_rows[s_first[at] + s_rank[s]] = s;
-        s_slot[at * 8 * NT + s / p.k] = (int16_t)s;
+        s_choice[at * 8 * NT + s / p.k] = (int8_t)(s % p.k);
+        atomicOr(&s_tiles[at], 1 << (s / p.k / 8));
     }
     if (p.fs)
-        for (int t = threadIdx.x; t < T; t += FT_THREADS) s_slot[A * 8 * NT + t] = (int16_t)(slots + t);
+        for (int t = threadIdx.x; t < T; t += FT_THREADS) {
+            s_choice[A * 8 * NT + t] = 0;
+            atomicOr(&s_tiles[A], 1 << (t / 8));
+        }
     __syncthreads();
 
-    // ---- gate|up ----
-    {
-        const int fb = p.f >> 3;
-        const int units = A * fb + (p.fs >> 3);
-        const int steps = (p.d + FT_KC - 1) / FT_KC;
-        // a warp's batches: unit u, steps c, c + 16, c + 32, c + 48
-        int u = blockIdx.x, c = warp;
-        const __nv_bfloat16 *lo = nullptr, *hi = nullptr;
-        auto rows_of = [&](int unit) {
-            if (unit < A * fb) {
-                const int a = unit / fb;
-                lo = p.w_gateup + ((size_t)s_active[a] * 2 * p.f + (unit - a * fb) * 8 + g) * p.d + t4 * 8;
-                hi = lo + (size_t)p.f * p.d;
-            } else {
-                lo = p.s_gateup + ((size_t)(unit - A * fb) * 8 + g) * p.d + t4 * 8;
-                hi = lo + (size_t)p.fs * p.d;
-            }
-        };
-        auto fetch = [&](int from, uint4 (&w)[FT_BATCH][2]) {
+    // The operands of a ring stage: A (weights) in slots 2m (MMA rows 0-7 of block m) and 2m + 1 (rows 8-15), B (the tokens'
+    // rows) in slot 4 + n.
+    float acc[2][NT][4];
+    auto clear = [&] {
 #pragma unroll
-            for (int i = 0; i < FT_BATCH; ++i) {
-                const int k0 = (from + i * FT_WARPS) * FT_KC;
-                w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
-                if (k0 + t4 * 8 < p.d) {
-                    w[i][0] = ld_weight(lo + k0);
-                    w[i][1] = ld_weight(hi + k0);
-                }
-            }
-        };
-        uint4 w[FT_BATCH][2], wn[FT_BATCH][2];
-        float acc[NT][4];
-        int turn = 0;
-        if (u < units) {
-            rows_of(u);
-            fetch(c, w);
-        }
-        bool fresh = true;
-        int count = 0, nt_used = 0;
-        const __nv_bfloat16* xr[NT];
-        while (u < units) {
-            if (fresh) {
-                const int a = u / fb;
-                const bool routed = u < A * fb;
-                count = routed ? s_first[a + 1] - s_first[a] : T;
-                nt_used = (count + 7) / 8;
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int col = n * 8 + g;
-                    xr[n] = nullptr;
-                    if (col < count) xr[n] = p.x + (size_t)(routed ? s_rows[s_first[a] + col] / p.k : col) * p.d + t4 * 8;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-                }
-            }
-            const int u0 = u, c0 = c;
-            c += FT_BATCH * FT_WARPS;
-            if (c >= steps) {
-                u += gridDim.x;
-                c = warp;
-                if (u < units) rows_of(u);
-            }
-            if (u < units) fetch(c, wn);
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+    };
+    auto multiply = [&](uint32_t at, int tiles) {  // one step from the stage at `at`
+        uint4 w[4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n >= nt_used) break;
-                uint4 b[FT_BATCH];
+        for (int i = 0; i < 4; ++i) w[i] = ld_shared_16(at + i * SLOT_BYTES);
 #pragma unroll
-                for (int i = 0; i < FT_BATCH; ++i) {
-                    const int k0 = (c0 + i * FT_WARPS) * FT_KC;
-                    b[i] = make_uint4(0, 0, 0, 0);
-                    if (xr[n] && k0 + t4 * 8 < p.d) b[i] = __ldg(reinterpret_cast<const uint4*>(xr[n] + k0));
-                }
+        for (int n = 0; n < NT; ++n) {
+            if (NT > 1 && !((tiles >> n) & 1)) continue;
+            const uint4 b = ld_shared_16(at + (4 + n) * SLOT_BYTES);
 #pragma unroll
-                for (int i = 0; i < FT_BATCH; ++i) {
-                    mma_bf16(acc[n], w[i][0].x, w[i][1].x, w[i][0].y, w[i][1].y, b[i].x, b[i].y);
-                    mma_bf16(acc[n], w[i][0].z, w[i][1].z, w[i][0].w, w[i][1].w, b[i].z, b[i].w);
-                }
-            }
-            fresh = u != u0;
-            if (fresh) {  // the unit's sums: through shared memory, then SwiGLU
-                float4* r = red + turn * RED;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    if (n < nt_used) r[(warp * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-                __syncthreads();
-                const float* rf = reinterpret_cast<const float*>(r);
-                for (int i = threadIdx.x; i < 64 * nt_used; i += FT_THREADS) {
-                    const int n = i >> 6, j = (i >> 3) & 7, col = i & 7;
-                    if (n * 8 + col >= count) continue;
-                    float gate = 0.f, up = 0.f;
-#pragma unroll
-                    for (int q = 0; q < FT_WARPS; ++q) {
-                        const float* v = rf + (((q * NT + n) * 32) + j * 4 + (col >> 1)) * 4 + (col & 1);
-                        gate += v[0];
-                        up += v[2];
-                    }
-                    const int a = u0 / fb;
-                    if (u0 < A * fb) {
-                        const int s = s_rows[s_first[a] + n * 8 + col];
-                        p.h[(size_t)s * p.ldh + (u0 - a * fb) * 8 + j] = __float2bfloat16_rn(s_w[s] * swiglu(gate, up));
-                    } else {
-                        p.h[(size_t)(slots + n * 8 + col) * p.ldh + (u0 - A * fb) * 8 + j] = __float2bfloat16_rn(swiglu(gate, up));
-                    }
-                }
-                turn ^= 1;
-            }
-#pragma unroll
-            for (int i = 0; i < FT_BATCH; ++i) {
-                w[i][0] = wn[i][0];
-                w[i][1] = wn[i][1];
-            }
-        }
-    }
-
-    // ---- down ----
-    const int fsteps = (p.f + FT_KC - 1) / FT_KC, ssteps = (p.fs + FT_KC - 1) / FT_KC;
-    const int per = A * fsteps + ssteps;  // steps of a block of 16 output columns
-    const int blocks = (p.d + 15) / 16;
-    const long all = (long)per * blocks;
-    const long r0 = all * blockIdx.x / gridDim.x, r1 = all * (blockIdx.x + 1) / gridDim.x;
-    // step s of column block cb -> this thread's weight pointers (null past the matrix) and k
-    auto fetch = [&](int cb, int s, int s_end, uint4 (&w)[FT_BATCH][2]) {
-#pragma unroll
-        for (int i = 0; i < FT_BATCH; ++i) {
-            const int st = s + i * FT_WARPS;
-            w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
-            if (st < s_end) {
-                const int a = min(st / fsteps, A);
-                const int K = a < A ? p.f : p.fs;
-                const int k = (st - a * fsteps) * FT_KC + t4 * 8;
-                if (k < K) {
-                    const __nv_bfloat16* m = a < A ? p.w_down + (size_t)s_active[a] * p.d * p.f : p.s_down;
-                    const int row = cb * 16 + g;
-                    w[i][0] = ld_weight(m + (size_t)row * K + k);
-                    if (row + 8 < p.d) w[i][1] = ld_weight(m + (size_t)(row + 8) * K + k);
-                }
+            for (int m = 0; m < 2; ++m) {
+                mma_bf16(acc[m][n], w[2 * m].x, w[2 * m + 1].x, w[2 * m].y, w[2 * m + 1].y, b.x, b.y);
+                mma_bf16(acc[m][n], w[2 * m].z, w[2 * m + 1].z, w[2 * m].w, w[2 * m + 1].w, b.z, b.w);
             }
         }
     };
-    uint4 w[FT_BATCH][2], wn[FT_BATCH][2];
-    int cb = (int)(r0 / per);
-    int s_begin = (int)(r0 - (long)cb * per), s_end = (int)min((long)per, s_begin + (r1 - r0));
-    const int cb_first = cb;
-    if (r0 < r1) fetch(cb, s_begin + warp, s_end, w);
-    if (!grid_barrier(p.counters, s_n + 1)) return;
-    int turn = 0;
-    int s = s_begin + warp;
-    float acc[NT][4] = {};
-    long left = r1 - r0;  // steps of the CTA's range from s_begin on
-    while (left > 0) {
-        // the next batch: of this column block, or the first of the next one
-        const int cb0 = cb, s0 = s, s_end0 = s_end, s_begin0 = s_begin;
-        const bool last = s_begin + FT_BATCH * FT_WARPS * ((s - s_begin) / (FT_BATCH * FT_WARPS) + 1) >= s_end;
-        s += FT_BATCH * FT_WARPS;
-        if (last) {
-            left -= s_end - s_begin;
-            ++cb;
-            s_begin = 0;
-            s_end = (int)min((long)per, left);
-            s = warp;
+    auto publish = [&](int tiles, int m0) {  // this warp's sums of blocks m0 .. m0 + RB - 1, for the CTA to add
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                if (m >= m0 && m < m0 + RB && (NT == 1 || (tiles >> n) & 1))
+                    red[((warp * RB + m - m0) * NT + n) * 32 + lane] =
+                        make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+    };
+    const float* rf = reinterpret_cast<const float*>(red);
+    // MMA row `row` (0-15) and column `col` of the m-th block in `red`, token block n, of warp q
+    auto element = [&](int q, int m, int n, int row, int col) {
+        return rf[((((q * RB + m) * NT + n) * 32) + (row & 7) * 4 + (col >> 1)) * 4 + (row >> 3) * 2 + (col & 1)];
+    };
+
+    // ---- gate|up ----
+    {
+        const int fb = (p.f + 15) >> 4, sb = (p.fs + 15) >> 4;
+        const int units = A * fb + sb;
+        const int steps = (p.d + FT_KC - 1) / FT_KC;
+        // step i of the CTA's n-th unit goes to warp (n steps + i) mod 16
+        auto first_step = [&](int n) { return (warp - n * steps) & (FT_WARPS - 1); };
+        // the copies run ahead of the sums: unit pu (the CTA's pn-th), step pc
+        int pu = blockIdx.x, pn = 0, pc = first_step(0), p_stage = 0, p_used = 0;
+        const __nv_bfloat16 *lo = nullptr, *x_row[NT];
+        size_t up = 0;       // from a gate row to its up row
+        bool second = false;  // the unit's second 8 columns exist
+        bool fresh = true;
+        auto issue = [&] {
+            while (pu < units && pc >= steps) {
+                pu += gridDim.x;
+                pc = first_step(++pn);
+                fresh = true;
+            }
+            if (pu < units) {
+                if (fresh) {
+                    fresh = false;
+                    const int a = pu / fb;
+                    const bool routed = pu < A * fb;
+                    const int j0 = (pu - (routed ? a : A) * fb) * 16, cols = routed ? p.f : p.fs;
+                    lo = (routed ? p.w_gateup + (size_t)s_active[a] * 2 * p.f * p.d : p.s_gateup) + (size_t)(j0 + g) * p.d + t4 * 8;
+                    up = (size_t)cols * p.d;
+                    second = j0 + 8 < cols;
+                    const int count = routed ? s_first[a + 1] - s_first[a] : T;
+                    p_used = (count + 7) / 8;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int col = n * 8 + g;
+                        x_row[n] = nullptr;
+                        if (col < count) x_row[n] = p.x + (size_t)(routed ? s_rows[s_first[a] + col] / p.k : col) * p.d + t4 * 8;
+                    }
+                }
+                const int k0 = pc * FT_KC;
+                const bool in = k0 + t4 * 8 < p.d;
+                const uint32_t to = ring + p_stage * STAGE_BYTES;
+                const __nv_bfloat16* row = lo + (in ? k0 : 0);
+                cp_async_16(to, row, in);
+                cp_async_16(to + SLOT_BYTES, row + up, in);
+                const size_t next8 = second ? (size_t)8 * p.d : 0;
+                cp_async_16(to + 2 * SLOT_BYTES, row + next8, in && second);
+                cp_async_16(to + 3 * SLOT_BYTES, row + next8 + up, in && second);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    if (n < p_used) cp_async_16(to + (4 + n) * SLOT_BYTES, x_row[n] ? x_row[n] + (in ? k0 : 0) : p.x, in && x_row[n]);
+                pc += FT_WARPS;
+            }
+            cp_async_commit();
+            if (++p_stage == STAGES) p_stage = 0;
+        };
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) issue();
+        int stage = 0;
+        for (int u = blockIdx.x, n_unit = 0; u < units; u += gridDim.x, ++n_unit) {
+            const int a = u / fb;
+            const bool routed = u < A * fb;
+            const int count = routed ? s_first[a + 1] - s_first[a] : T;
+            const int used = (count + 7) / 8, tiles = (1 << used) - 1;
+            clear();
+            for (int c = first_step(n_unit); c < steps; c += FT_WARPS) {
+                issue();  // into the stage of the step before
+                cp_async_wait<STAGES - 1>();
+                multiply(ring + stage * STAGE_BYTES, tiles);
+                if (++stage == STAGES) stage = 0;
+            }
+#pragma unroll
+            for (int m0 = 0; m0 < 2; m0 += RB) {
+                publish(tiles, m0);
+                __syncthreads();
+                for (int i = threadIdx.x; i < 64 * RB * used; i += FT_THREADS) {
+                    const int n = i / (64 * RB), m = (i >> 6) % RB, j = (i >> 3) & 7, col = i & 7;
+                    const int j0 = (u - (routed ? a : A) * fb) * 16 + (m0 + m) * 8 + j;
+                    if (n * 8 + col >= count || j0 >= (routed ? p.f : p.fs)) continue;
+                    float gate = 0.f, upv = 0.f;
+#pragma unroll
+                    for (int q = 0; q < FT_WARPS; ++q) {
+                        gate += element(q, m, n, j, col);
+                        upv += element(q, m, n, j + 8, col);
+                    }
+                    float h = swiglu(gate, upv);
+                    int s = slots + n * 8 + col;
+                    if (routed) {
+                        s = s_rows[s_first[a] + n * 8 + col];
+                        h *= s_w[s];
+                    }
+                    p.h[(size_t)s * p.ldh + j0] = __float2bfloat16_rn(h);
+                }
+                __syncthreads();
+            }
         }
-        if (left > 0) fetch(cb, s, s_end, wn);
-        uint4 b[FT_BATCH];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int i = 0; i < FT_BATCH; ++i) {
-                const int st = s0 + i * FT_WARPS;
-                b[i] = make_uint4(0, 0, 0, 0);
-                if (st < s_end0) {
-                    const int a = min(st / fsteps, A);
-                    const int k = (st - a * fsteps) * FT_KC + t4 * 8;
-                    const int slot = s_slot[a * 8 * NT + n * 8 + g];
-                    if (slot >= 0 && k < (a < A ? p.f : p.fs))
-                        b[i] = *reinterpret_cast<const uint4*>(p.h + (size_t)slot * p.ldh + k);
+        cp_async_wait<0>();
+    }
+
+    // ---- down ----
+    {
+        const int fsteps = (p.f + FT_KC - 1) / FT_KC, ssteps = (p.fs + FT_KC - 1) / FT_KC;
+        const int per = A * fsteps + ssteps;  // steps of a block of 32 output columns
+        const int blocks = (p.d + 31) / 32;
+        const int all = per * blocks;
+        const int r0 = (int)((long)all * blockIdx.x / gridDim.x), r1 = (int)((long)all * (blockIdx.x + 1) / gridDim.x);
+        // where step r lies: column block cb, active expert a (A: the shared one), K step c; 16 further on
+        struct Place {
+            int cb, a, c;
+        };
+        auto place = [&](int r) {
+            Place at;
+            at.cb = r / per;
+            const int s = r - at.cb * per;
+            at.a = min(s / fsteps, A);
+            at.c = s - at.a * fsteps;
+            return at;
+        };
+        auto advance = [&](Place& at) {
+            at.c += FT_WARPS;
+            for (int len = at.a < A ? fsteps : ssteps; at.c >= len; len = at.a < A ? fsteps : ssteps) {
+                at.c -= len;
+                if (++at.a > A) {  // past the shared expert's (perhaps no) steps
+                    at.a = 0;
+                    ++at.cb;
                 }
             }
+        };
+        auto issue_weights = [&](const Place& at, int stage) {
+            const int K = at.a < A ? p.f : p.fs, k = at.c * FT_KC + t4 * 8, row = at.cb * 32 + g;
+            const __nv_bfloat16* m = at.a < A ? p.w_down + (size_t)s_active[at.a] * p.d * p.f : p.s_down;
+            const uint32_t to = ring + stage * STAGE_BYTES;
 #pragma unroll
-            for (int i = 0; i < FT_BATCH; ++i) {
-                mma_bf16(acc[n], w[i][0].x, w[i][1].x, w[i][0].y, w[i][1].y, b[i].x, b[i].y);
-                mma_bf16(acc[n], w[i][0].z, w[i][1].z, w[i][0].w, w[i][1].w, b[i].z, b[i].w);
+            for (int i = 0; i < 4; ++i) {
+                const bool in = k < K && row + 8 * i < p.d;
+                cp_async_16(to + i * SLOT_BYTES, in ? m + (size_t)(row + 8 * i) * K + k : p.x, in);
             }
-        }
-        if (last) {
-            float4* r = red + turn * RED;
-            turn ^= 1;
+        };
+        auto issue_h = [&](const Place& at, int stage) {
+            const int K = at.a < A ? p.f : p.fs, k = at.c * FT_KC + t4 * 8;
+            const int tiles = s_tiles[at.a];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                r[(warp * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+                if (NT > 1 && !((tiles >> n) & 1)) continue;
+                const int choice = s_choice[at.a * 8 * NT + n * 8 + g];
+                const int slot = at.a < A ? (n * 8 + g) * p.k + choice : slots + n * 8 + g;
+                const bool in = choice >= 0 && k < K;
+                cp_async_16(ring + stage * STAGE_BYTES + (4 + n) * SLOT_BYTES, in ? p.h + (size_t)slot * p.ldh + k : p.h, in);
             }
-            __syncthreads();
-            const float* rf = reinterpret_cast<const float*>(r);
-            const bool whole = s_begin0 == 0 && s_end0 == per;
-            constexpr int OUT = 128 * NT;  // (column, token) values: i = token * 16 + column
-            float* mine = p.part + ((size_t)blockIdx.x * 2 + (cb0 == cb_first ? 0 : 1)) * OUT;
-            for (int i = threadIdx.x; i < OUT; i += FT_THREADS) {
-                const int t = i >> 4, col = i & 15;
-                float v = 0.f;
+        };
+        int pr = r0 + warp;
+        Place ahead = place(min(pr, all - 1)), at = ahead;
+        {
+            Place b = ahead;
 #pragma unroll
-                for (int q = 0; q < FT_WARPS; ++q)
-                    v += rf[(((q * NT + (t >> 3)) * 32) + (col & 7) * 4 + ((t & 7) >> 1)) * 4 + (col >> 3) * 2 + (t & 1)];
-                if (!whole)
-                    mine[i] = v;
-                else if (t < T && cb0 * 16 + col < p.d)
-                    p.y[(size_t)t * p.d + cb0 * 16 + col] = __float2bfloat16_rn(v);
+            for (int i = 0; i < STAGES - 1; ++i) {
+                if (pr + i * FT_WARPS < r1) {
+                    issue_weights(b, i);
+                    advance(b);
+                }
+                cp_async_commit();
+            }
+        }
+        if (!grid_barrier(p.counters, s_n + 1)) {
+            cp_async_wait<0>();
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) {
+            if (pr < r1) {
+                issue_h(ahead, i);
+                advance(ahead);
+            }
+            pr += FT_WARPS;
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        int stage = 0, p_stage = STAGES - 1;
+        int r = r0 + warp;
+        const int cb_first = r0 / per;
+        for (int cb = cb_first, begin = r0; begin < r1; ++cb) {
+            const int end = (int)min((long)r1, (long)(cb + 1) * per);
+            clear();
+            for (; r < end; r += FT_WARPS) {
+                if (pr < r1) {
+                    issue_weights(ahead, p_stage);
+                    issue_h(ahead, p_stage);
+                    advance(ahead);
+                }
+                cp_async_commit();
+                pr += FT_WARPS;
+                if (++p_stage == STAGES) p_stage = 0;
+                cp_async_wait<STAGES - 1>();
+                multiply(ring + stage * STAGE_BYTES, s_tiles[at.a]);
+                advance(at);
+                if (++stage == STAGES) stage = 0;
+            }
+            const bool whole = end - begin == per;
+            constexpr int OUT = 256 * NT;  // (token, column) values: i = token * 32 + column
+            float* mine = p.part + ((size_t)blockIdx.x * 2 + (cb == cb_first ? 0 : 1)) * OUT;
+#pragma unroll
+            for (int m0 = 0; m0 < 2; m0 += RB) {
+                publish((1 << NT) - 1, m0);
+                __syncthreads();
+                for (int i = threadIdx.x; i < 128 * RB * NT; i += FT_THREADS) {
+                    const int t = i / (16 * RB), col = i % (16 * RB), c = m0 * 16 + col;
+                    if (t >= T || cb * 32 + c >= p.d) continue;
+                    float v = 0.f;
+#pragma unroll
+                    for (int q = 0; q < FT_WARPS; ++q) v += element(q, col >> 4, t >> 3, col & 15, t & 7);
+                    if (whole)
+                        p.y[(size_t)t * p.d + cb * 32 + c] = __float2bfloat16_rn(v);
+                    else
+                        mine[t * 32 + c] = v;
+                }
+                if (m0 + RB < 2) __syncthreads();
             }
             if (!whole) {  // cut between CTAs: the last one to arrive adds the parts in their order
-                const long x0 = (long)cb0 * per, x1 = x0 + per - 1;
+                const long x0 = (long)cb * per, x1 = x0 + per - 1;
                 const int b0 = (int)(((x0 + 1) * gridDim.x - 1) / all), b1 = (int)(((x1 + 1) * gridDim.x - 1) / all);
                 __threadfence();
                 __syncthreads();
-                if (threadIdx.x == 0) s_n[1] = atomicAdd(p.counters + 1 + cb0, 1) == b1 - b0;
+                if (threadIdx.x == 0) s_n[1] = atomicAdd(p.counters + 1 + cb, 1) == b1 - b0;
                 __syncthreads();
                 if (s_n[1]) {
                     __threadfence();
                     for (int i = threadIdx.x; i < OUT; i += FT_THREADS) {
-                        const int t = i >> 4, col = i & 15;
+                        const int t = i >> 5, col = i & 31;
+                        if (t >= T || cb * 32 + col >= p.d) continue;
                         float v = 0.f;
                         for (int q = b0; q <= b1; ++q) {
-                            const int which = (int)(all * q / gridDim.x / per) == cb0 ? 0 : 1;
+                            const int which = (int)((long)all * q / gridDim.x) / per == cb ? 0 : 1;
                             v += __ldcg(p.part + ((size_t)q * 2 + which) * OUT + i);
                         }
-                        if (t < T && cb0 * 16 + col < p.d) p.y[(size_t)t * p.d + cb0 * 16 + col] = __float2bfloat16_rn(v);
+                        p.y[(size_t)t * p.d + cb * 32 + col] = __float2bfloat16_rn(v);
                     }
                 }
-                __syncthreads();
             }
+            __syncthreads();
+            begin = end;
         }
-#pragma unroll
-        for (int i = 0; i < FT_BATCH; ++i) {
-            w[i][0] = wn[i][0];
-            w[i][1] = wn[i][1];
-        }
+        cp_async_wait<0>();
     }
 }
 

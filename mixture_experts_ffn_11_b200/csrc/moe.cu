@@ -802,17 +802,18 @@ struct FewWorkspace {  // byte offsets: counters | h | parts
 };
 FewWorkspace few_workspace(int T, int d, int f, int fs, int k) {
     FewWorkspace w;
-    w.n_counters = 1 + (d + 15) / 16;
+    w.n_counters = 1 + (d + 31) / 32;
     w.ldh = f > fs ? f : fs;
     w.h = ((size_t)w.n_counters * 4 + 255) / 256 * 256;
     w.part = w.h + ((size_t)(T * k + (fs ? T : 0)) * w.ldh * 2 + 255) / 256 * 256;
-    w.bytes = w.part + (size_t)FT_MAX_CTAS * 2 * 16 * (T <= 8 ? 8 : (T <= 16 ? 16 : 32)) * 4;
+    w.bytes = w.part + (size_t)FT_MAX_CTAS * 2 * 32 * (T <= 8 ? 8 : (T <= 16 ? 16 : 32)) * 4;
     return w;
 }
 
 template <int NT>
 size_t few_smem(int slots, int E) {
-    return (size_t)2 * FT_WARPS * NT * 32 * 16 + (size_t)FewTables::words(slots, E) * 4 + (size_t)(slots + 1) * 8 * NT * 2;
+    return (size_t)FT_STAGES<NT> * (4 + NT) * FT_THREADS * 16 + (size_t)FT_WARPS * FT_RED_BLOCKS<NT> * NT * 32 * 16 +
+           (size_t)FewTables::words(slots, E) * 4 + (size_t)(slots + 1) * 8 * NT;
 }
 
 cudaError_t set_few_attributes() {
@@ -1610,7 +1611,7 @@ moe_status_t moe_few_tokens(const moe_bf16_t* x, const float* w_router, const fl
                                logits_out, a.counters, w.n_counters);
     if ((st = check_launch("few_tokens (logits)", e)) != MOE_OK) return st;
     // at least one step of the down projection per CTA (some expert is always active)
-    const long steps = (long)((f + FT_KC - 1) / FT_KC) * ((d + 15) / 16);
+    const long steps = (long)((f + FT_KC - 1) / FT_KC) * ((d + 31) / 32);
     const int grid = (int)std::min<long>(steps, std::min(di.sms, FT_MAX_CTAS));
     if (T <= 8)
         e = launch_few<1>(a, grid, stream);
