@@ -6,13 +6,15 @@ Python binding (``_native``) plus a layer object that owns buffers and calls the
 """
 from . import _native
 from ._native import (MoEError, ROUTE_MODES, block_norm_backward_workspace_size, block_norm_in, block_norm_in_backward,
-                      block_norm_out, block_norm_out_backward, few_tokens, few_tokens_workspace_size,
-                      fp8_block_quantize, fp8_row_quantize, get_device_error, grouped_gemm_down, grouped_gemm_down_fp8, grouped_gemm_gateup, grouped_gemm_gateup_fp8, permute,
-                      permute_workspace_size, route_topk, topk_from_logits, unpermute_combine)
-from .layer import MoEFFN
+                      block_norm_out, block_norm_out_backward, few_tokens, few_tokens_workspace_size, fp8_block_quantize,
+                      fp8_row_quantize, get_device_error, grouped_gemm_down, grouped_gemm_down_fp8, grouped_gemm_gateup,
+                      grouped_gemm_gateup_fp8, permute, permute_workspace_size, route_topk, topk_from_logits,
+                      unpermute_combine)
+from .layer import MoEBlock, MoEFFN
 
-__all__ = ["MoEFFN", "MoEError", "ROUTE_MODES", "route_topk", "topk_from_logits", "permute",
+__all__ = ["MoEFFN", "MoEBlock", "MoEError", "ROUTE_MODES", "route_topk", "topk_from_logits", "permute",
            "permute_workspace_size", "grouped_gemm_gateup", "grouped_gemm_down", "unpermute_combine",
-           "block_norm_in", "block_norm_out", "block_norm_in_backward", "block_norm_out_backward",
-           "block_norm_backward_workspace_size", "few_tokens", "few_tokens_workspace_size", "fp8_block_quantize", "fp8_row_quantize", "grouped_gemm_gateup_fp8",
-           "grouped_gemm_down_fp8", "get_device_error"]
+           "few_tokens", "few_tokens_workspace_size", "fp8_block_quantize", "fp8_row_quantize",
+           "grouped_gemm_gateup_fp8", "grouped_gemm_down_fp8", "block_norm_in", "block_norm_out",
+           "block_norm_in_backward", "block_norm_out_backward", "block_norm_backward_workspace_size",
+           "get_device_error"]

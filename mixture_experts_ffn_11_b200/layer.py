@@ -32,6 +32,24 @@ def _encode_mxfp4(*ws):
     return q, s
 
 
+def _encode_fp8(w, halves: int):
+    """bf16 weights [G, N, K] -> (e4m3 [G, N, K], scales per 128 x 128 block [G, halves, ceil(N/halves/128), ceil(K/128)]);
+    halves = 2 for gate|up, which are blocked apart. A pair (e4m3, scales) is taken as it is."""
+    G, n, K = (w[0] if isinstance(w, tuple) else w).shape
+    shape = (G, halves, N.fp8_blocks(n // halves), N.fp8_blocks(K))
+    shape = shape if halves > 1 else (shape[0],) + shape[2:]
+    if isinstance(w, tuple):
+        q, s = w
+        if q.dtype != N.E4M3 or s.dtype != torch.float32 or tuple(s.shape) != shape:
+            raise ValueError(f"want (float8_e4m3fn {(G, n, K)}, float32 {shape}), got ({q.dtype}, {s.dtype} {tuple(s.shape)})")
+        return q, s
+    q = torch.empty(G, n, K, dtype=N.E4M3, device=w.device)
+    s = torch.empty(shape, dtype=torch.float32, device=w.device)
+    N.fp8_block_quantize(w.view(G * halves, n // halves, K), q.view(G * halves, n // halves, K),
+                         s.view(G * halves, *shape[-2:]))
+    return q, s
+
+
 class MoEFFN:
     """One MoE feed-forward layer with packed expert weights.
 
@@ -39,7 +57,10 @@ class MoEFFN:
     bias [E] fp32 or None; optional shared expert w_gateup_shared [2fs, d], w_down_shared [d, fs].
     weights: "bf16" keeps the expert weights as given; "mxfp4" encodes them once (moe_mxfp4_quantize, 4.25 bits
     per weight) and the layer then computes with the weights the encoding represents, through the MXFP4 grouped
-    GEMMs; the bf16 tensors are not kept.
+    GEMMs; the bf16 tensors are not kept. "fp8" encodes them once as e4m3 with a scale per 128 x 128 block
+    (moe_fp8_block_quantize), or takes them so encoded, each weight given as a pair (e4m3 values, scales); the rows
+    that enter each product are encoded on the way, with a scale per 128 columns (moe_fp8_row_quantize). d and f are
+    multiples of 16 then.
     fused: with bf16 weights and groups of 128 rows or more on average (prefill), let the dispatch and the
     collect steps ride in the grouped GEMMs: the gate|up GEMM reads its rows straight from x through perm_src
     (moe_grouped_gemm_gateup_gather) instead of a grouped copy x_perm made by moe_permute, and the down GEMM's
@@ -52,25 +73,31 @@ class MoEFFN:
     summed without rounding). Not used by a training forward, whose backward pass reads the separate calls' buffers.
     """
 
+    few = False
+
     def __init__(self, w_router, w_gateup, w_down, k: int, route: str = "topk_softmax", bias=None,
                  w_gateup_shared=None, w_down_shared=None, weights: str = "bf16", fused: bool = False,
                  few: bool = False):
         self.E, self.d = w_router.shape
-        self.f = w_gateup.shape[1] // 2
+        first = w_gateup[0] if isinstance(w_gateup, tuple) else w_gateup
+        self.f = first.shape[1] // 2
         self.k = k
         self.route = route
         if route not in N.ROUTE_MODES:
             raise ValueError(f"unknown routing mode {route!r}")
-        if weights not in ("bf16", "mxfp4"):
+        if weights not in ("bf16", "mxfp4", "fp8"):
             raise ValueError(f"unknown weight format {weights!r}")
+        if isinstance(w_gateup, tuple) and weights != "fp8":
+            raise ValueError('encoded weights are for weights="fp8"')
         self.weights = weights
         self.fused = fused
         self.few = few
         self._x_perm_valid = False
         self.w_router, self.w_gateup, self.w_down, self.bias = w_router, w_gateup, w_down, bias
         self.w_gateup_shared, self.w_down_shared = w_gateup_shared, w_down_shared
-        self.shared_f = w_gateup_shared.shape[0] // 2 if w_gateup_shared is not None else 0
-        self.device = w_gateup.device
+        shared = w_gateup_shared[0] if isinstance(w_gateup_shared, tuple) else w_gateup_shared
+        self.shared_f = shared.shape[-2] // 2 if shared is not None else 0
+        self.device = first.device
         # MXFP4 with a shared expert as wide as a routed one: its weights are encoded as group E of the routed
         # tensors; for decode-sized T (_fold) its T rows (x itself) follow the R routed rows, and the routed GEMM
         # launches compute it as one more group, spread over every SM like the rest (on its own it is one group of
@@ -91,6 +118,13 @@ class MoEFFN:
                 if self.shared_f:
                     self.mx_gateup_shared = _encode_mxfp4(w_gateup_shared.unsqueeze(0))
                     self.mx_down_shared = _encode_mxfp4(w_down_shared.unsqueeze(0))
+            self.w_gateup = self.w_down = self.w_gateup_shared = self.w_down_shared = None
+        elif weights == "fp8":
+            self.f8 = {"gateup": _encode_fp8(w_gateup, 2), "down": _encode_fp8(w_down, 1)}
+            if self.shared_f:  # one group; given encoded, a pair has that group's dimension
+                one = lambda w: w if isinstance(w, tuple) else w.unsqueeze(0)  # noqa: E731
+                self.f8["gateup_shared"] = _encode_fp8(one(w_gateup_shared), 2)
+                self.f8["down_shared"] = _encode_fp8(one(w_down_shared), 1)
             self.w_gateup = self.w_down = self.w_gateup_shared = self.w_down_shared = None
         self._T = None
         self.buf = {}
@@ -132,7 +166,7 @@ class MoEFFN:
             "offsets": torch.empty(E + 1, dtype=i32, device=dev),
             "perm_src": torch.empty(R, dtype=i32, device=dev),
             "inv_perm": torch.empty(R, dtype=i32, device=dev),
-            "x_perm": torch.empty(R, d, dtype=bf, device=dev),
+            "x_perm": torch.empty(R if self.weights != "fp8" else 0, d, dtype=bf, device=dev),
             "h": torch.empty(R, f, dtype=bf, device=dev),
             "y_perm": torch.empty(R, d, dtype=bf, device=dev),
             "ws": torch.empty(max(N.permute_workspace_size(T, E, k), 256), dtype=torch.uint8, device=dev),
@@ -155,6 +189,12 @@ class MoEFFN:
             b["shared_offsets"] = torch.tensor([0, T], dtype=i32, device=dev)
             b["h_shared"] = torch.empty(T, self.shared_f, dtype=bf, device=dev)
             b["shared"] = torch.empty(T, d, dtype=bf, device=dev)
+        if self.weights == "fp8":  # the rows entering each product: e4m3 values and scales
+            def rows(n, K):
+                return (torch.empty(n, K, dtype=N.E4M3, device=dev), torch.empty(N.fp8_blocks(K), n, dtype=f32, device=dev))
+            b["xq"], b["hq"] = rows(R, d), rows(R, f)
+            if self.shared_f:
+                b["xq_shared"], b["hq_shared"] = rows(T, d), rows(T, self.shared_f)
         self.buf, self._T = b, T
         return b
 
@@ -203,6 +243,8 @@ class MoEFFN:
             if self._fold(T):  # its rows after the routed ones; the routed GEMMs compute it
                 N.gather_rows(x, b["shared_rows"], b["x_perm_all"][T * self.k:], side)
             else:
+                if self.weights == "fp8":
+                    N.fp8_row_quantize(x, None, *b["xq_shared"], side)
                 self._gateup(x, "shared", b["shared_offsets"], b["h_shared"], side)
                 self._down(b["h_shared"], "shared", b["shared_offsets"], b["shared"], side)
             shared_done = torch.cuda.Event()
@@ -221,13 +263,15 @@ class MoEFFN:
         save = train and self.weights == "bf16"
         self._gu_saved = False
         mark("permute", True)
-        if fused:  # grouping only; the gate|up GEMM gathers its rows from x
+        if fused or self.weights == "fp8":  # grouping only; the gate|up GEMM, or the encoder, gathers its rows from x
             N.permute(None, b["topk_idx"], self.E, b["counts"], b["offsets"], b["perm_src"], b["inv_perm"], None,
                       b["ws"], s)
+            if not fused:
+                N.fp8_row_quantize(x, b["perm_src"], *b["xq"], s)
         else:
             N.permute(x, b["topk_idx"], self.E, b["counts"], b["offsets"], b["perm_src"], b["inv_perm"], b["x_perm"],
                       b["ws"], s)
-        self._x_perm_valid = not fused
+        self._x_perm_valid = not fused and self.weights != "fp8"
         mark("permute", False)
         if shared is not None:
             # the routed GEMMs are persistent kernels sized to every SM: they start once the shared expert is done
@@ -295,6 +339,10 @@ class MoEFFN:
         if self.weights == "mxfp4":
             q, sc = self.mx_gateup if which == "routed" else self.mx_gateup_shared
             N.grouped_gemm_gateup_mxfp4(a, q, sc, offsets, h, stream)
+        elif self.weights == "fp8":  # of the rows encoded before
+            shared = which == "shared"
+            N.grouped_gemm_gateup_fp8(*self.buf["xq_shared" if shared else "xq"],
+                                      *self.f8["gateup_shared" if shared else "gateup"], offsets, h, stream)
         else:
             w = self.w_gateup if which == "routed" else self.w_gateup_shared.unsqueeze(0)
             N.grouped_gemm_gateup(a, w, offsets, h, stream)
@@ -303,6 +351,11 @@ class MoEFFN:
         if self.weights == "mxfp4":
             q, sc = self.mx_down if which == "routed" else self.mx_down_shared
             N.grouped_gemm_down_mxfp4(h, q, sc, offsets, y, stream)
+        elif self.weights == "fp8":
+            shared = which == "shared"
+            hq = self.buf["hq_shared" if shared else "hq"]
+            N.fp8_row_quantize(h, None, *hq, stream)
+            N.grouped_gemm_down_fp8(*hq, *self.f8["down_shared" if shared else "down"], offsets, y, stream)
         else:
             w = self.w_down if which == "routed" else self.w_down_shared.unsqueeze(0)
             N.grouped_gemm_down(h, w, offsets, y, stream)
@@ -465,7 +518,8 @@ class MoEFFN:
         tensor-core path with fused top-k is taken (E <= 128, T >= 2048), else logits + top-k;
         permute 4, gate|up, down, combine 1 each (fused: permute 3, gate|up 1, down with combine 1; train: the
         gate|up that keeps its pre-activations is 1 kernel with 128 rows or more per expert, else 2); the shared
-        expert 2 more (1 folded: the copy of its rows). few: 2 in all where it is taken."""
+        expert 2 more (1 folded: the copy of its rows). fp8: one more, which encodes h (the gather encodes x), and 2
+        more for the shared expert. few: 2 in all where it is taken."""
         if T <= 0:
             return 0
         if self._few(T) and not train:
@@ -475,4 +529,89 @@ class MoEFFN:
             body = 4 + 3 + (0 if T * self.k >= 128 * self.E else 1)
         else:
             body = 3 + 2 if self._fused(T) else 4 + 3
+        if self.weights == "fp8":
+            return route + body + 1 + (4 if self.shared_f else 0)
         return route + body + ((1 if self._fold(T) else 2) if self.shared_f else 0)
+
+
+class MoEBlock:
+    """A residual block around a MoEFFN: the "dense feed-forward block" of a transformer backbone with its norms and residual
+    (blog post "Mixture of Experts (MoEs) in Transformers", section "From Dense to Sparse").
+
+        out = alpha * r + gate * (w_out * norm(ffn(w_in * norm(r)))),  norm(v) = v / sqrt(mean(v^2) + eps)
+
+    ffn: the MoEFFN; w_in, w_out [d] fp32 gains; gate: None, or a learned gate [d] bf16 (forward() also takes one per call); alpha
+    the residual scale. The residual stream r is bf16 or fp32 [T, d]. Blocks in a row pass the next one's normed input on, made in
+    the same pass as the residual: out, xn = a(r, next_norm=b.w_in); out = b(out, xn=xn).
+    """
+
+    def __init__(self, ffn: MoEFFN, w_in, w_out, gate=None, alpha: float = 1.0, eps: float = 1e-6):
+        if w_in.shape != (ffn.d,) or w_out.shape != (ffn.d,) or (gate is not None and gate.shape != (ffn.d,)):
+            raise ValueError(f"w_in, w_out and gate are vectors of d = {ffn.d}")
+        self.ffn, self.w_in, self.w_out, self.gate, self.alpha, self.eps = ffn, w_in, w_out, gate, alpha, eps
+        self._key, self._buf, self._call = None, {}, None
+
+    def _buffers(self, T: int, dtype) -> dict:
+        """Outputs and kept values, allocated once per T and type of the stream."""
+        if self._key != (T, dtype):
+            d, dev = self.ffn.d, self.ffn.device
+            new = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=dev)  # noqa: E731
+            self._buf = {"xn": new(T, d, t=torch.bfloat16), "rstd_in": new(T), "out": new(T, d, t=dtype), "rstd": new(T),
+                         "xn_next": new(T, d, t=torch.bfloat16), "rstd_next": new(T)}
+            self._key = (T, dtype)
+        return self._buf
+
+    def forward(self, r, xn=None, next_norm=None, gate=None, gate_rows: int = 0, train: bool = False, stream=None):
+        """The block's output stream [T, d] (a buffer of the block), or with next_norm (the next block's w_in) the pair (output
+        stream, its normed input for the next block). xn: this block's normed input, if the block before made it. gate [ceil(T /
+        gate_rows), d] bf16: a gate for this call, one row per gate_rows tokens. train: keep what backward() reads."""
+        T = r.shape[0]
+        b = self._buffers(T, r.dtype)
+        if gate is None and self.gate is not None:
+            gate, gate_rows = self.gate.view(1, -1)[:min(T, 1)], max(T, 1)
+        made = xn is None
+        if made:
+            xn = b["xn"]
+            N.block_norm_in(r, self.w_in, self.eps, xn, b["rstd_in"], stream)
+        y = self.ffn.forward(xn, stream, train=train)
+        N.block_norm_out(y, r, self.w_out, gate, gate_rows, self.alpha, next_norm, self.eps, b["out"], b["rstd"],
+                         b["xn_next"] if next_norm is not None else None, b["rstd_next"] if next_norm is not None else None, stream)
+        self._call = (r, y, gate, gate_rows, next_norm, made)
+        return b["out"] if next_norm is None else (b["out"], b["xn_next"])
+
+    __call__ = forward
+
+    def backward(self, dout, dxn=None, weight_grads: bool = True, stream=None) -> dict:
+        """Gradients of the last forward(train=True) for the output stream's gradient dout [T, d] (type of the stream) and, where
+        the next block's norm was part of it, dxn [T, d] bf16, the gradient of the normed input made for that block.
+
+        Returns MoEFFN.backward's gradients (of the expert and router weights) and "dr" (of r), "dw_out", "dgate" (rows of the gate,
+        fp32, or None), "dw_next" (of next_norm, or None), and "dw_in"; where xn was given to forward(), "dw_in" is None and "dxn"
+        is xn's gradient, both of which the block before takes: a.backward(g["dr"], g["dxn"])."""
+        if self._call is None:
+            raise RuntimeError("backward() follows a forward()")
+        r, y, gate, gate_rows, next_norm, made = self._call
+        b, f = self._buf, self.ffn
+        T, d = r.shape
+        key = (T, r.dtype, gate_rows)
+        if getattr(self, "_gkey", None) != key:
+            new = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=f.device)  # noqa: E731
+            ws = N.block_norm_backward_workspace_size(T, d, gate_rows)
+            self._gbuf = {"dr": new(T, d, t=r.dtype), "dy": new(T, d, t=torch.bfloat16), "dw_out": new(d), "dw_in": new(d),
+                          "dw_next": new(d), "dgate": new(-(-T // gate_rows), d) if gate_rows else None,
+                          "ws": new(max(ws, 16), t=torch.uint8)}
+            self._gkey = key
+        g = self._gbuf
+        nxt = next_norm is not None
+        N.block_norm_out_backward(dout, dxn, y, b["out"] if nxt else None, self.w_out, gate, gate_rows, self.alpha, next_norm,
+                                  b["rstd"], b["rstd_next"] if nxt else None, g["dr"], g["dy"], g["dw_out"], g["dgate"],
+                                  g["dw_next"] if nxt else None, g["ws"], stream)
+        out = dict(f.backward(g["dy"], weight_grads=weight_grads, stream=stream))
+        dx = out.pop("dx")
+        if made:
+            N.block_norm_in_backward(dx, g["dr"], r, self.w_in, b["rstd_in"], g["dr"], g["dw_in"], g["ws"], stream)
+        else:
+            out["dxn"] = dx
+        out.update(dr=g["dr"], dw_out=g["dw_out"], dgate=g["dgate"], dw_in=g["dw_in"] if made else None,
+                   dw_next=g["dw_next"] if nxt else None)
+        return out
