@@ -9,6 +9,10 @@
 // Each is one pass over its arrays (a few flops per element, so HBM bounds it). A row belongs to one CTA, whose threads
 // hold VPT vectors of 8 columns each, the same columns for every row: the gains stay in registers, and the gradients of
 // gains and gate, sums over rows, are kept there too until the CTA's rows are done. Sums are in fp32.
+//
+// Many rows: they arrive in shared memory by bulk copies that run BN stages ahead (RowRing), so HBM does not wait for a row's
+// reductions; a stage is refilled as soon as the CTA has its row in registers. Few rows (at most one per CTA): plain loads, without
+// the copies' extra latency.
 #pragma once
 #include "common.cuh"
 
@@ -60,7 +64,102 @@ struct Vec8<float> {
 constexpr int BN_MAX_THREADS = 512;
 constexpr int BN_MAX_WARPS = BN_MAX_THREADS / 32;
 constexpr int BN_MAX_D = BN_MAX_THREADS * 4 * 8;  // 4 vectors per thread
+constexpr int BN_MAX_STAGES = 8;
 constexpr int BN_GRAD_CTAS = 296;  // rows of a backward pass are cut into at most so many ranges (2 per SM)
+
+// One of the arrays that make up a row's input: row t is the `bytes` from base + t / per * bytes (per > 1: a gate row shared by
+// consecutive tokens).
+struct RowArray {
+    const void* base;
+    uint32_t bytes;
+    int per;
+};
+
+// Ring of rows in shared memory. RING = false: the same interface on the arrays themselves.
+template <bool RING, int NARR>
+struct RowRing {
+    RowArray arr[NARR];
+    uint64_t* full;
+    volatile int* abort_flag;
+    uint8_t* data;
+    uint32_t row_bytes;
+    int stages, stage, step, end, next;  // next: the row to copy next
+    uint32_t phase;
+    uint64_t limit;
+    int row;
+
+    // rows first, first + step, ... < end
+    __device__ __forceinline__ void start(uint8_t* smem, int n_stages, int first, int step_, int end_) {
+        step = step_;
+        end = end_;
+        row = first - step_;
+        next = first;
+        if constexpr (RING) {
+            full = reinterpret_cast<uint64_t*>(smem);
+            abort_flag = reinterpret_cast<volatile int*>(full + BN_MAX_STAGES);
+            data = smem + 128;
+            stages = n_stages;
+            stage = -1;
+            phase = 1;
+            limit = wait_limit_ns();
+            row_bytes = 0;
+#pragma unroll
+            for (int i = 0; i < NARR; ++i) row_bytes += arr[i].bytes;
+            if (threadIdx.x == 0) {
+                for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+                *abort_flag = 0;
+                fence_mbar_init();
+                for (int s = 0; s < stages; ++s) copy(s);
+            }
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ void copy(int s) {  // the next row into stage s (one thread)
+        if (next >= end || *abort_flag) return;
+        mbar_arrive_expect_tx(&full[s], row_bytes);
+        uint8_t* to = data + (size_t)s * row_bytes;
+#pragma unroll
+        for (int i = 0; i < NARR; ++i) {
+            if (arr[i].bytes == 0) continue;
+            const int r = arr[i].per > 1 ? next / arr[i].per : next;
+            bulk_load(to, reinterpret_cast<const uint8_t*>(arr[i].base) + (size_t)r * arr[i].bytes, arr[i].bytes, &full[s]);
+            to += arr[i].bytes;
+        }
+        next += step;
+    }
+    // Go on to the next row, once it has arrived; false behind the last. (A wait that runs out sets the error bit and the rows
+    // that follow are computed from whatever is there: no thread leaves alone.)
+    __device__ __forceinline__ bool advance() {
+        row += step;
+        if (row >= end) return false;
+        if constexpr (RING) {
+            if (++stage == stages) stage = 0;
+            if (stage == 0) phase ^= 1u;
+            mbar_wait_within(&full[stage], phase, abort_flag, limit);
+        }
+        return true;
+    }
+    // Elements of array i of the current row
+    template <typename E>
+    __device__ __forceinline__ const E* get(int i) const {
+        if constexpr (RING) {
+            uint32_t at = 0;
+#pragma unroll
+            for (int j = 0; j < NARR; ++j)
+                if (j < i) at += arr[j].bytes;
+            return reinterpret_cast<const E*>(data + (size_t)stage * row_bytes + at);
+        } else {
+            const int r = arr[i].per > 1 ? row / arr[i].per : row;
+            return reinterpret_cast<const E*>(reinterpret_cast<const uint8_t*>(arr[i].base) + (size_t)r * arr[i].bytes);
+        }
+    }
+    // The CTA has the current row in registers (all its threads are past a barrier since): its stage takes another
+    __device__ __forceinline__ void release() {
+        if constexpr (RING) {
+            if (threadIdx.x == 0) copy(stage);
+        }
+    }
+};
 
 // Sums of NS values over the CTA, given to every thread. `red` is one of two alternating buffers, so one barrier per call
 // suffices: a thread that is a call ahead writes the other buffer, and two calls ahead is past the next barrier.
@@ -97,25 +196,31 @@ __device__ __forceinline__ void load_gains(const float* w, int nvec, float (&g)[
 
 // ---- forward ----------------------------------------------------------------------------------------
 
-template <typename R, int VPT>
+template <typename R, int VPT, bool RING>
 __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_kernel(const R* __restrict__ x, const float* __restrict__ w, int T,
                                                              int d, float eps, __nv_bfloat16* __restrict__ xn,
-                                                             float* __restrict__ rstd) {
+                                                             float* __restrict__ rstd, int stages) {
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][1][BN_MAX_WARPS];
     grid_dep_wait();
     grid_dep_trigger();
     const int nvec = d >> 3;
+    RowRing<RING, 1> rows;
+    rows.arr[0] = {x, (uint32_t)(d * sizeof(R)), 1};
+    rows.start(smem, stages, blockIdx.x, gridDim.x, T);
     float g[VPT][8];
     load_gains<VPT>(w, nvec, g);
     int turn = 0;
-    for (int t = blockIdx.x; t < T; t += gridDim.x, turn ^= 1) {
+    for (; rows.advance(); turn ^= 1) {
+        const int t = rows.row;
+        const R* x_row = rows.template get<R>(0);
         Vec8<R> q[VPT];
         float s[1] = {0.f};
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
             const int v = threadIdx.x + u * blockDim.x;
             q[u].zero();
-            if (v < nvec) q[u].load(x + (size_t)t * d + (size_t)v * 8);
+            if (v < nvec) q[u].load(x_row + v * 8);
         }
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
@@ -125,6 +230,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_kernel(const R* 
             for (int i = 0; i < 8; ++i) s[0] = fmaf(f[i], f[i], s[0]);
         }
         block_sums<1>(s, red[turn]);
+        rows.release();
         const float rs = rsqrtf(s[0] / (float)d + eps);
         if (threadIdx.x == 0) rstd[t] = rs;
 #pragma unroll
@@ -156,23 +262,30 @@ struct NormOutArgs {
     float alpha, eps;
 };
 
-template <typename R, int VPT, bool NEXT>
-__global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_kernel(const NormOutArgs a) {
+template <typename R, int VPT, bool NEXT, bool RING>
+__global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_kernel(const NormOutArgs a, int stages) {
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][1][BN_MAX_WARPS];
     grid_dep_wait();
     grid_dep_trigger();
     const int nvec = a.d >> 3;
+    RowRing<RING, 3> rows;
+    rows.arr[0] = {a.y, (uint32_t)(a.d * 2), 1};
+    rows.arr[1] = {a.r, (uint32_t)(a.d * sizeof(R)), 1};
+    rows.arr[2] = {a.gate, a.gate ? (uint32_t)(a.d * 2) : 0u, a.gate_rows};
+    rows.start(smem, stages, blockIdx.x, gridDim.x, a.T);
     float g[VPT][8], gn[NEXT ? VPT : 1][8];
     load_gains<VPT>(a.w, nvec, g);
     if constexpr (NEXT) load_gains<VPT>(a.w_next, nvec, gn);
-    const R* r = reinterpret_cast<const R*>(a.r);
     R* out = reinterpret_cast<R*>(a.out);
     int turn = 0;
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    while (rows.advance()) {
+        const int t = rows.row;
         Vec8<__nv_bfloat16> y[VPT], gt[VPT];
         Vec8<R> q[VPT];
         float s[1] = {0.f};
-        const size_t grow = a.gate ? (size_t)(t / a.gate_rows) * a.d : 0;
+        const __nv_bfloat16 *y_row = rows.template get<__nv_bfloat16>(0), *gate_row = rows.template get<__nv_bfloat16>(2);
+        const R* r_row = rows.template get<R>(1);
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
             const int v = threadIdx.x + u * blockDim.x;
@@ -180,9 +293,9 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_kernel(const No
             q[u].zero();
             gt[u].zero();
             if (v < nvec) {
-                y[u].load(a.y + (size_t)t * a.d + (size_t)v * 8);
-                q[u].load(r + (size_t)t * a.d + (size_t)v * 8);
-                if (a.gate) gt[u].load(a.gate + grow + (size_t)v * 8);
+                y[u].load(y_row + v * 8);
+                q[u].load(r_row + v * 8);
+                if (a.gate) gt[u].load(gate_row + v * 8);
             }
         }
 #pragma unroll
@@ -193,6 +306,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_kernel(const No
             for (int i = 0; i < 8; ++i) s[0] = fmaf(f[i], f[i], s[0]);
         }
         block_sums<1>(s, red[turn]);
+        rows.release();
         turn ^= 1;
         const float rs = rsqrtf(s[0] / (float)a.d + a.eps);
         if (threadIdx.x == 0) a.rstd[t] = rs;
@@ -246,7 +360,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_kernel(const No
 // the same bits every time. A gate row whose tokens all lie in one CTA is written there; of the others a CTA can only
 // have its first and its last (slots 0 and 1).
 
-__device__ __forceinline__ int norm_first_row(int T, int B, int b) { return (int)((long)T * b / B); }
+__host__ __device__ __forceinline__ int norm_first_row(int T, int B, int b) { return (int)((long)T * b / B); }
 
 struct NormInGradArgs {
     const __nv_bfloat16* dxn;  // [T][d]
@@ -259,23 +373,29 @@ struct NormInGradArgs {
     int T, d;
 };
 
-template <typename R, int VPT>
-__global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_grad_kernel(const NormInGradArgs a) {
+template <typename R, int VPT, bool RING>
+__global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_grad_kernel(const NormInGradArgs a, int stages) {
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][1][BN_MAX_WARPS];
     const int nvec = a.d >> 3;
     const float inv_d = 1.f / (float)a.d;
+    RowRing<RING, 3> rows;
+    rows.arr[0] = {a.dxn, (uint32_t)(a.d * 2), 1};
+    rows.arr[1] = {a.x, (uint32_t)(a.d * sizeof(R)), 1};
+    rows.arr[2] = {a.dres, a.dres ? (uint32_t)(a.d * sizeof(R)) : 0u, 1};
+    rows.start(smem, stages, norm_first_row(a.T, gridDim.x, blockIdx.x), 1, norm_first_row(a.T, gridDim.x, blockIdx.x + 1));
     float g[VPT][8], acc[VPT][8];
     load_gains<VPT>(a.w, nvec, g);
 #pragma unroll
     for (int u = 0; u < VPT; ++u)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[u][i] = 0.f;
-    const R* x = reinterpret_cast<const R*>(a.x);
-    const R* dres = reinterpret_cast<const R*>(a.dres);
     R* dx = reinterpret_cast<R*>(a.dx);
     int turn = 0;
-    const int t1 = norm_first_row(a.T, gridDim.x, blockIdx.x + 1);
-    for (int t = norm_first_row(a.T, gridDim.x, blockIdx.x); t < t1; ++t, turn ^= 1) {
+    for (; rows.advance(); turn ^= 1) {
+        const int t = rows.row;
+        const __nv_bfloat16* dxn_row = rows.template get<__nv_bfloat16>(0);
+        const R *x_row = rows.template get<R>(1), *dres_row = rows.template get<R>(2);
         Vec8<__nv_bfloat16> dn[VPT];
         Vec8<R> q[VPT], res[VPT];
         float s[1] = {0.f};
@@ -287,10 +407,9 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_grad_kernel(cons
             q[u].zero();
             res[u].zero();
             if (v < nvec) {
-                const size_t at = (size_t)t * a.d + (size_t)v * 8;
-                dn[u].load(a.dxn + at);
-                q[u].load(x + at);
-                if (dres) res[u].load(dres + at);
+                dn[u].load(dxn_row + v * 8);
+                q[u].load(x_row + v * 8);
+                if (a.dres) res[u].load(dres_row + v * 8);
             }
         }
 #pragma unroll
@@ -306,6 +425,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_grad_kernel(cons
             }
         }
         block_sums<1>(s, red[turn]);
+        rows.release();
         const float mean = s[0] * inv_d;
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
@@ -356,14 +476,23 @@ struct NormOutGradArgs {
 //   dy = rstd (dR g w - yhat S2 / d),                  S2 = sum dR g w yhat,  yhat = y rstd
 // S2 needs dR, which needs S1; but it is linear in it: S2 = SA - (rstd'^3 S1 / d) SB with SA = sum (dout + rstd' dxn w') g w
 // yhat and SB = sum out g w yhat, so one reduction over the row gives all three. dR is never rounded.
-template <typename R, int VPT, bool NEXT, bool GATE>
-__global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(const NormOutGradArgs a) {
+template <typename R, int VPT, bool NEXT, bool GATE, bool RING>
+__global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(const NormOutGradArgs a, int stages) {
     constexpr int NS = NEXT ? 3 : 1;
+    extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float red[2][NS][BN_MAX_WARPS];
     const int nvec = a.d >> 3;
     const float inv_d = 1.f / (float)a.d;
     float g[VPT][8], gn[NEXT ? VPT : 1][8];
     float acc[VPT][8], acc_next[NEXT ? VPT : 1][8], acc_gate[GATE ? VPT : 1][8];
+    const int t0 = norm_first_row(a.T, gridDim.x, blockIdx.x), t1 = norm_first_row(a.T, gridDim.x, blockIdx.x + 1);
+    RowRing<RING, 5> rows;
+    rows.arr[0] = {a.dout, (uint32_t)(a.d * sizeof(R)), 1};
+    rows.arr[1] = {a.y, (uint32_t)(a.d * 2), 1};
+    rows.arr[2] = {a.out, NEXT ? (uint32_t)(a.d * sizeof(R)) : 0u, 1};
+    rows.arr[3] = {a.dxn, NEXT ? (uint32_t)(a.d * 2) : 0u, 1};
+    rows.arr[4] = {a.gate, GATE ? (uint32_t)(a.d * 2) : 0u, a.gate_rows};
+    rows.start(smem, stages, t0, 1, t1);
     load_gains<VPT>(a.w, nvec, g);
     if constexpr (NEXT) load_gains<VPT>(a.w_next, nvec, gn);
 #pragma unroll
@@ -374,12 +503,10 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
             if constexpr (NEXT) acc_next[u][i] = 0.f;
             if constexpr (GATE) acc_gate[u][i] = 0.f;
         }
-    const R* dout = reinterpret_cast<const R*>(a.dout);
-    const R* out = reinterpret_cast<const R*>(a.out);
     R* dr = reinterpret_cast<R*>(a.dr);
     int turn = 0;
-    const int t0 = norm_first_row(a.T, gridDim.x, blockIdx.x), t1 = norm_first_row(a.T, gridDim.x, blockIdx.x + 1);
-    for (int t = t0; t < t1; ++t, turn ^= 1) {
+    for (; rows.advance(); turn ^= 1) {
+        const int t = rows.row;
         Vec8<__nv_bfloat16> dn[NEXT ? VPT : 1], y[VPT], gt[GATE ? VPT : 1];
         Vec8<R> up[VPT], o[NEXT ? VPT : 1];
         float s[NS] = {};
@@ -394,14 +521,13 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
             if constexpr (NEXT) o[u].zero(), dn[u].zero();
             if constexpr (GATE) gt[u].zero();
             if (v < nvec) {
-                const size_t at = (size_t)t * a.d + (size_t)v * 8;
-                up[u].load(dout + at);
-                y[u].load(a.y + at);
+                up[u].load(rows.template get<R>(0) + v * 8);
+                y[u].load(rows.template get<__nv_bfloat16>(1) + v * 8);
                 if constexpr (NEXT) {
-                    o[u].load(out + at);
-                    dn[u].load(a.dxn + at);
+                    o[u].load(rows.template get<R>(2) + v * 8);
+                    dn[u].load(rows.template get<__nv_bfloat16>(3) + v * 8);
                 }
-                if constexpr (GATE) gt[u].load(a.gate + (size_t)group * a.d + (size_t)v * 8);
+                if constexpr (GATE) gt[u].load(rows.template get<__nv_bfloat16>(4) + v * 8);
             }
         }
 #pragma unroll
@@ -426,6 +552,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
             }
         }
         block_sums<NS>(s, red[turn]);
+        rows.release();
         float c = 0.f;  // dR = dout + rstd' dxn w' - c out
         if constexpr (NEXT) c = rn * rn * rn * s[1] * inv_d;
         const float mean = (NEXT ? s[0] - c * s[NS - 1] : s[0]) * inv_d;
@@ -489,54 +616,42 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
     }
 }
 
-// Adds up what the CTAs left: blockIdx.y = 0: dw, 1: dw_next, 2 + b: the gate row that holds the boundary between the
-// rows of CTA b and CTA b + 1, unless an earlier boundary lies in it too. 32 columns per block; warp i adds the partial
-// rows i, i + 8, ..., then warp 0 adds the eight sums in order.
+// Adds up what the CTAs left: blockIdx.y = 0: dw, 1: dw_next (with part_next), then the gate rows that lie in several CTAs, each by
+// the first CTA whose last row is one of its tokens but not the last (edge: that CTA). 32 columns per block; warp i adds the
+// partial rows i, i + 16, ..., then warp 0 adds the sixteen sums in order.
 struct NormReduceArgs {
     const float *part_w, *part_next, *part_gate;
     float *dw, *dw_next, *dgate;
-    int T, d, gate_rows, B;
+    int T, d, gate_rows, B, sums;  // sums: 1, or 2 with part_next
+    int16_t edge[BN_GRAD_CTAS];
 };
 
-constexpr int BNR_WARPS = 8;
+constexpr int BNR_WARPS = 16;
 
-__global__ void __launch_bounds__(BNR_WARPS * 32) block_norm_reduce_kernel(const NormReduceArgs a) {
+__global__ void __launch_bounds__(BNR_WARPS * 32) block_norm_reduce_kernel(const __grid_constant__ NormReduceArgs a) {
     __shared__ float sums[BNR_WARPS][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * 32 + lane;
     const int job = blockIdx.y;
     int b0 = 0, b1 = a.B;  // CTAs to add
-    long group = 0;
-    float* to;
-    if (job == 0) {
-        to = a.dw;
-    } else if (job == 1) {
-        if (!a.part_next) return;
-        to = a.dw_next;
-    } else {
-        const int b = job - 2;
-        const int edge = norm_first_row(a.T, a.B, b + 1);
-        group = edge / a.gate_rows;
-        const long g0 = group * a.gate_rows, g1 = min(g0 + a.gate_rows, (long)a.T);
-        if (edge == g0 || norm_first_row(a.T, a.B, b) > g0) return;  // no tokens before the edge; an earlier edge's group
-        b0 = b;
-        b1 = b + 2;
-        while (b1 < a.B && norm_first_row(a.T, a.B, b1) < g1) ++b1;
+    const float* from = job == 0 ? a.part_w : a.part_next;
+    float* to = job == 0 ? a.dw : a.dw_next;
+    size_t pitch = a.d;
+    int slot0 = 0;  // of a gate row in the first CTA: 1 if that CTA has an earlier gate row in part too
+    if (job >= a.sums) {
+        b0 = a.edge[job - a.sums];
+        const long group = (norm_first_row(a.T, a.B, b0 + 1) - 1) / a.gate_rows;
+        const long last = min((group + 1) * a.gate_rows, (long)a.T) - 1;
+        b1 = (int)(((last + 1) * a.B - 1) / a.T) + 1;  // one past the CTA of the last token
+        slot0 = norm_first_row(a.T, a.B, b0) / a.gate_rows == group ? 0 : 1;
+        from = a.part_gate;
         to = a.dgate + group * a.d;
+        pitch *= 2;
     }
     float s = 0.f;
     if (col < a.d) {
-#pragma unroll 4
-        for (int b = b0 + warp; b < b1; b += BNR_WARPS) {
-            const float* from;
-            if (job == 0)
-                from = a.part_w + (size_t)b * a.d;
-            else if (job == 1)
-                from = a.part_next + (size_t)b * a.d;
-            else
-                from = a.part_gate + ((size_t)b * 2 + (norm_first_row(a.T, a.B, b) / a.gate_rows == group ? 0 : 1)) * a.d;
-            s += from[col];
-        }
+#pragma unroll 8
+        for (int b = b0 + warp; b < b1; b += BNR_WARPS) s += from[b * pitch + (b == b0 ? (size_t)slot0 * a.d : 0) + col];
     }
     sums[warp][lane] = s;
     __syncthreads();

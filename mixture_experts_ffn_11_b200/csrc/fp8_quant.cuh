@@ -17,37 +17,60 @@ namespace moe {
 constexpr int F8_BLOCK = 128;
 constexpr float F8_MAX = 448.f;
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+
 struct F8Scaler {
-    float c, m, r, scale;
+    uint64_t c, minus_m, r;  // each twice
+    float scale;
     __device__ __forceinline__ explicit F8Scaler(float top) {
         const bool some = top > 0.f;
         // p = 2^k with top * p near 1 (its exponent kept where p, 448 p and 1 / (top p) are normal numbers)
         const int e = min(max((int)(__float_as_uint(top) >> 23) & 255, 16), 252);
         const float p = __uint_as_float((uint32_t)(254 - e) << 23);
-        c = p * F8_MAX;
-        m = some ? top * p : 1.f;
-        r = __frcp_rn(m);
+        const float m = some ? top * p : 1.f;
+        const float rcp = __frcp_rn(m);
+        c = pair2(p * F8_MAX, p * F8_MAX);
+        minus_m = pair2(-m, -m);
+        r = pair2(rcp, rcp);
         scale = some ? __fdiv_rn(top, F8_MAX) : 1.f;
     }
-    __device__ __forceinline__ float quotient(float x) const {
-        const float a = x * c;
-        const float q = a * r;
-        return fmaf(fmaf(-q, m, a), r, q);
+    // two bf16 values -> two e4m3 bytes
+    __device__ __forceinline__ uint32_t two(uint32_t v) const {
+        const uint64_t a = mul2(pair2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)), c);
+        const uint64_t q = mul2(a, r);
+        const uint64_t out = fma2(fma2(q, minus_m, a), r, q);
+        float lo, hi;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(out));
+        return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
     }
-    __device__ __forceinline__ uint32_t pair(float x0, float x1) const {
-        return __nv_cvt_float2_to_fp8x2(make_float2(quotient(x0), quotient(x1)), __NV_SATFINITE, __NV_E4M3);
-    }
-    // 8 bf16 values -> 8 e4m3 bytes
     __device__ __forceinline__ uint2 eight(const uint4& v) const {
-        const float2 f0 = unpack_bf16x2(v.x), f1 = unpack_bf16x2(v.y), f2 = unpack_bf16x2(v.z), f3 = unpack_bf16x2(v.w);
-        return make_uint2(pair(f0.x, f0.y) | pair(f1.x, f1.y) << 16, pair(f2.x, f2.y) | pair(f3.x, f3.y) << 16);
+        return make_uint2(two(v.x) | two(v.y) << 16, two(v.z) | two(v.w) << 16);
     }
 };
 
+// The largest magnitude of 8 bf16 values (a NaN counts only beside another).
 __device__ __forceinline__ float top_of(const uint4& v) {
-    const float2 f0 = unpack_bf16x2(v.x), f1 = unpack_bf16x2(v.y), f2 = unpack_bf16x2(v.z), f3 = unpack_bf16x2(v.w);
-    return fmaxf(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))),
-                 fmaxf(fmaxf(fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y))));
+    const auto abs2 = [](uint32_t u) {
+        u &= 0x7fff7fffu;
+        return *reinterpret_cast<const __nv_bfloat162*>(&u);
+    };
+    const __nv_bfloat162 m = __hmax2(__hmax2(abs2(v.x), abs2(v.y)), __hmax2(abs2(v.z), abs2(v.w)));
+    return fmaxf(__low2float(m), __high2float(m));
 }
 
 // Rows of x (row r of the output is row row_src[r] of x [T][K], or row r without row_src): q [R][K], s [ceil(K/128)][R].

@@ -122,13 +122,10 @@ __device__ __forceinline__ void tmem_wait_ld(float (&a)[16], float (&b)[16]) {
                  : "memory");
 }
 
-// acc += {v0, v1} * s, two fp32 multiply-adds in one instruction
-__device__ __forceinline__ void fma2(float2& acc, float v0, float v1, const float2& s) {
-    asm("{\n\t.reg .b64 a, v, s;\n\t"
-        "mov.b64 a, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\t"
-        "fma.rn.f32x2 a, v, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "+f"(acc.x), "+f"(acc.y)
-        : "f"(v0), "f"(v1), "f"(s.x), "f"(s.y));
+// acc += {v0, v1} * s
+__device__ __forceinline__ void fma2_acc(float2& acc, float v0, float v1, const float2& s) {
+    const uint64_t r = fma2(pair2(v0, v1), pair2(s.x, s.y), pair2(acc.x, acc.y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(acc.x), "=f"(acc.y) : "l"(r));
 }
 
 // Register shares of the warpgroups (setmaxnreg): the block is launched with 384 x 168 = 64,512 registers, which the
@@ -580,8 +577,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const int r = 4 * j + 2 * i;
-                                fma2(acc[2 * b + (j >> 1)][0][2 * (j & 1) + i], v[b & 1][0][r], v[b & 1][0][r + 1], s0[j]);
-                                fma2(acc[2 * b + (j >> 1)][1][2 * (j & 1) + i], v[b & 1][1][r], v[b & 1][1][r + 1], s1[j]);
+                                fma2_acc(acc[2 * b + (j >> 1)][0][2 * (j & 1) + i], v[b & 1][0][r], v[b & 1][0][r + 1], s0[j]);
+                                fma2_acc(acc[2 * b + (j >> 1)][1][2 * (j & 1) + i], v[b & 1][1][r], v[b & 1][1][r + 1], s1[j]);
                             }
                     }
                     if constexpr (NB == 0) {

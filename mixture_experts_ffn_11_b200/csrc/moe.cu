@@ -918,16 +918,41 @@ moe_status_t gemm_fp8(const uint8_t* a, const float* sa, const uint8_t* w, const
 // ---- block norms ----
 namespace {
 
-// Threads and vectors per thread for rows of d columns. Few rows (a decoding step): one vector per thread where that fits,
-// for the shortest path through a row.
+// Launch shape for T rows of d columns, row_bytes of input each: vectors per thread, threads, CTAs and stages of the row ring
+// (0: no ring). Up to two rows per SM: a row per CTA by plain loads, one vector per thread where that fits, for the shortest path
+// through a row. More: rings that fill about 200 KB of shared memory per SM between `per_sm` CTAs.
 struct NormShape {
-    int vpt, threads;
+    int vpt, threads, grid, stages;
+    size_t smem;
 };
-NormShape norm_shape(int T, int d, int sms) {
+constexpr size_t kNormRingBytes = 204 * 1024;
+NormShape norm_shape(int T, int d, int sms, size_t row_bytes, int vpt1_max, int per_sm) {
     const int nvec = d / 8;
-    int vpt = nvec <= 128 ? 1 : (nvec <= 2 * BN_MAX_THREADS ? 2 : 4);
-    if (T <= sms && nvec <= BN_MAX_THREADS) vpt = 1;
-    return {vpt, (nvec + vpt * 32 - 1) / (vpt * 32) * 32};
+    NormShape s{};
+    const bool ring = T > 2 * sms;
+    s.vpt = nvec <= vpt1_max ? 1 : (nvec <= 2 * BN_MAX_THREADS ? 2 : 4);
+    if (!ring && nvec <= BN_MAX_THREADS) s.vpt = 1;
+    s.threads = (nvec + s.vpt * 32 - 1) / (s.vpt * 32) * 32;
+    if (!ring) {
+        s.grid = T;
+        return s;
+    }
+    int m = per_sm;
+    while (m > 1 && (m * s.threads > 1536 || 2 * row_bytes > kNormRingBytes / m)) --m;
+    s.grid = m * sms < T ? m * sms : T;
+    s.stages = (int)std::min<size_t>(BN_MAX_STAGES, (kNormRingBytes / m - 256) / row_bytes);
+    if (s.stages < 1) {  // rows too wide for a ring
+        s.stages = 0;
+        return s;
+    }
+    s.smem = 128 + (size_t)s.stages * row_bytes;
+    return s;
+}
+
+template <typename... KArgs>
+cudaError_t norm_smem(void (*kernel)(KArgs...), size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 moe_status_t check_norm_sizes(int T, int d, moe_stream_type_t type) {
@@ -953,69 +978,105 @@ moe_status_t check_norm_gate(const void* gate, int gate_rows, int T) {
 
 int norm_grad_ctas(int T) { return T < BN_GRAD_CTAS ? T : BN_GRAD_CTAS; }
 
-#define MOE_NORM_VPT(vpt, CALL)        \
-    switch (vpt) {                     \
-        case 1: CALL(1); break;        \
-        case 2: CALL(2); break;        \
-        default: CALL(4); break;       \
+#define MOE_NORM_CASES(s, CALL)                              \
+    if (s.stages) {                                          \
+        switch (s.vpt) {                                     \
+            case 1: CALL(1, true); break;                    \
+            case 2: CALL(2, true); break;                    \
+            default: CALL(4, true); break;                   \
+        }                                                    \
+    } else {                                                 \
+        switch (s.vpt) {                                     \
+            case 1: CALL(1, false); break;                   \
+            case 2: CALL(2, false); break;                   \
+            default: CALL(4, false); break;                  \
+        }                                                    \
     }
 
 template <typename R>
 cudaError_t launch_norm_in(const void* x, const float* w, int T, int d, float eps, void* xn, float* rstd, int sms,
                            cudaStream_t stream) {
-    const NormShape s = norm_shape(T, d, sms);
-    const int grid = grid_cap(T, sms, std::max(1, 1536 / s.threads));
+    const NormShape s = norm_shape(T, d, sms, (size_t)d * sizeof(R), 128, 4);
     cudaError_t e = cudaSuccess;
-#define CALL(V)                                                                                                   \
-    e = launch_pdl(block_norm_in_kernel<R, V>, dim3(grid), dim3(s.threads), 0, stream, reinterpret_cast<const R*>(x), w, T, d, \
-                   eps, reinterpret_cast<__nv_bfloat16*>(xn), rstd)
-    MOE_NORM_VPT(s.vpt, CALL)
+#define CALL(V, RING)                                                                                                      \
+    e = norm_smem(block_norm_in_kernel<R, V, RING>, s.smem);                                                               \
+    if (e == cudaSuccess)                                                                                                  \
+    e = launch_pdl(block_norm_in_kernel<R, V, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream,                        \
+                   reinterpret_cast<const R*>(x), w, T, d, eps, reinterpret_cast<__nv_bfloat16*>(xn), rstd, s.stages)
+    MOE_NORM_CASES(s, CALL)
 #undef CALL
     return e;
 }
 
 template <typename R, bool NEXT>
 cudaError_t launch_norm_out(const NormOutArgs& a, int sms, cudaStream_t stream) {
-    const NormShape s = norm_shape(a.T, a.d, sms);
-    const int grid = grid_cap(a.T, sms, std::max(1, 1024 / s.threads));
+    const NormShape s = norm_shape(a.T, a.d, sms, (size_t)a.d * (2 + sizeof(R) + (a.gate ? 2 : 0)), 128, 2);
     cudaError_t e = cudaSuccess;
-#define CALL(V) e = launch_pdl(block_norm_out_kernel<R, V, NEXT>, dim3(grid), dim3(s.threads), 0, stream, a)
-    MOE_NORM_VPT(s.vpt, CALL)
+#define CALL(V, RING)                                                                                                \
+    e = norm_smem(block_norm_out_kernel<R, V, NEXT, RING>, s.smem);                                                  \
+    if (e == cudaSuccess)                                                                                            \
+    e = launch_pdl(block_norm_out_kernel<R, V, NEXT, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream, a, s.stages)
+    MOE_NORM_CASES(s, CALL)
 #undef CALL
     return e;
 }
 
+// The backward kernels' grids: at most BN_GRAD_CTAS (the workspace has that many partial rows).
+NormShape norm_grad_shape(int T, int d, int sms, size_t row_bytes, int per_sm) {
+    NormShape s = norm_shape(T, d, sms, row_bytes, BN_MAX_THREADS, per_sm);
+    if (s.grid > BN_GRAD_CTAS) s.grid = BN_GRAD_CTAS;
+    return s;
+}
+
 template <typename R>
-cudaError_t launch_norm_in_grad(const NormInGradArgs& a, int sms, cudaStream_t stream) {
-    const NormShape s = norm_shape(a.T, a.d, sms);
+cudaError_t launch_norm_in_grad(const NormInGradArgs& a, int sms, cudaStream_t stream, int& B) {
+    const NormShape s = norm_grad_shape(a.T, a.d, sms, (size_t)a.d * (2 + sizeof(R) * (a.dres ? 2 : 1)), 2);
+    B = s.grid;
     cudaError_t e = cudaSuccess;
-#define CALL(V) e = launch_plain(block_norm_in_grad_kernel<R, V>, dim3(norm_grad_ctas(a.T)), dim3(s.threads), 0, stream, a)
-    MOE_NORM_VPT(s.vpt, CALL)
+#define CALL(V, RING)                                                                                                    \
+    e = norm_smem(block_norm_in_grad_kernel<R, V, RING>, s.smem);                                                        \
+    if (e == cudaSuccess)                                                                                                \
+    e = launch_plain(block_norm_in_grad_kernel<R, V, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream, a, s.stages)
+    MOE_NORM_CASES(s, CALL)
 #undef CALL
     return e;
 }
 
 template <typename R, bool NEXT, bool GATE>
-cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int sms, cudaStream_t stream) {
-    const NormShape s = norm_shape(a.T, a.d, sms);
+cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int sms, cudaStream_t stream, int& B) {
+    const NormShape s = norm_grad_shape(a.T, a.d, sms, (size_t)a.d * ((NEXT ? 2 : 1) * (2 + sizeof(R)) + (GATE ? 2 : 0)), 1);
+    B = s.grid;
     cudaError_t e = cudaSuccess;
-#define CALL(V) \
-    e = launch_plain(block_norm_out_grad_kernel<R, V, NEXT, GATE>, dim3(norm_grad_ctas(a.T)), dim3(s.threads), 0, stream, a)
-    MOE_NORM_VPT(s.vpt, CALL)
+#define CALL(V, RING)                                                                                                       \
+    e = norm_smem(block_norm_out_grad_kernel<R, V, NEXT, GATE, RING>, s.smem);                                              \
+    if (e == cudaSuccess)                                                                                                   \
+    e = launch_plain(block_norm_out_grad_kernel<R, V, NEXT, GATE, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream, a,  \
+                     s.stages)
+    MOE_NORM_CASES(s, CALL)
 #undef CALL
     return e;
 }
 
 template <typename R>
-cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int sms, cudaStream_t stream) {
+cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int sms, cudaStream_t stream, int& B) {
     if (a.dxn)
-        return a.gate ? launch_norm_out_grad<R, true, true>(a, sms, stream) : launch_norm_out_grad<R, true, false>(a, sms, stream);
-    return a.gate ? launch_norm_out_grad<R, false, true>(a, sms, stream) : launch_norm_out_grad<R, false, false>(a, sms, stream);
+        return a.gate ? launch_norm_out_grad<R, true, true>(a, sms, stream, B) : launch_norm_out_grad<R, true, false>(a, sms, stream, B);
+    return a.gate ? launch_norm_out_grad<R, false, true>(a, sms, stream, B) : launch_norm_out_grad<R, false, false>(a, sms, stream, B);
 }
 
-cudaError_t launch_norm_reduce(const NormReduceArgs& a, cudaStream_t stream) {
-    return launch_plain(block_norm_reduce_kernel, dim3((a.d + 31) / 32, a.part_gate ? a.B + 1 : 2), dim3(BNR_WARPS * 32), 0, stream,
-                        a);
+cudaError_t launch_norm_reduce(NormReduceArgs& a, cudaStream_t stream) {
+    a.sums = a.part_next ? 2 : 1;
+    int edges = 0;
+    if (a.part_gate) {
+        long seen = -1;  // gate row of the last edge
+        for (int b = 0; b + 1 < a.B; ++b) {
+            const int row = norm_first_row(a.T, a.B, b + 1);  // the first row behind CTA b
+            const long group = row / a.gate_rows;
+            if (row % a.gate_rows != 0 && group != seen) a.edge[edges++] = (int16_t)b;
+            if (row % a.gate_rows != 0) seen = group;
+        }
+    }
+    return launch_plain(block_norm_reduce_kernel, dim3((a.d + 31) / 32, a.sums + edges), dim3(BNR_WARPS * 32), 0, stream, a);
 }
 
 // Workspace of a backward pass: part_w [B][d] | part_next [B][d] | part_gate [B][2][d] (with a gate)
@@ -1738,13 +1799,14 @@ moe_status_t moe_block_norm_in_backward(const moe_bf16_t* dxn, const void* dres,
         return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
     }
     const NormInGradArgs a{reinterpret_cast<const __nv_bfloat16*>(dxn), dres, x, w, rstd, dx, reinterpret_cast<float*>(ws), T, d};
-    cudaError_t e = type == MOE_STREAM_FP32 ? launch_norm_in_grad<float>(a, di.sms, stream)
-                                            : launch_norm_in_grad<__nv_bfloat16>(a, di.sms, stream);
+    int B = 0;
+    cudaError_t e = type == MOE_STREAM_FP32 ? launch_norm_in_grad<float>(a, di.sms, stream, B)
+                                            : launch_norm_in_grad<__nv_bfloat16>(a, di.sms, stream, B);
     if ((st = check_launch("block_norm_in_backward", e)) != MOE_OK) return st;
     NormReduceArgs ra{};
     ra.part_w = a.part_w;
     ra.dw = dw;
-    ra.T = T, ra.d = d, ra.B = norm_grad_ctas(T);
+    ra.T = T, ra.d = d, ra.B = B;
     return check_launch("block_norm_in_backward (sums)", launch_norm_reduce(ra, stream));
 }
 
@@ -1774,7 +1836,7 @@ moe_status_t moe_block_norm_out_backward(const void* dout, const moe_bf16_t* dxn
         if (e == cudaSuccess && dw_next) e = cudaMemsetAsync(dw_next, 0, sizeof(float) * (size_t)d, stream);
         return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
     }
-    const int B = norm_grad_ctas(T);
+    int B = norm_grad_ctas(T);
     float* part = reinterpret_cast<float*>(ws);
     NormOutGradArgs a{};
     a.dout = dout, a.dxn = reinterpret_cast<const __nv_bfloat16*>(dxn), a.y = reinterpret_cast<const __nv_bfloat16*>(y);
@@ -1782,8 +1844,8 @@ moe_status_t moe_block_norm_out_backward(const void* dout, const moe_bf16_t* dxn
     a.rstd = rstd, a.rstd_next = rstd_next, a.dr = dr, a.dy = reinterpret_cast<__nv_bfloat16*>(dy), a.dgate = dgate;
     a.part_w = part, a.part_next = part + (size_t)B * d, a.part_gate = part + (size_t)2 * B * d;
     a.T = T, a.d = d, a.gate_rows = gate_rows, a.alpha = alpha;
-    cudaError_t e = type == MOE_STREAM_FP32 ? launch_norm_out_grad<float>(a, di.sms, stream)
-                                            : launch_norm_out_grad<__nv_bfloat16>(a, di.sms, stream);
+    cudaError_t e = type == MOE_STREAM_FP32 ? launch_norm_out_grad<float>(a, di.sms, stream, B)
+                                            : launch_norm_out_grad<__nv_bfloat16>(a, di.sms, stream, B);
     if ((st = check_launch("block_norm_out_backward", e)) != MOE_OK) return st;
     NormReduceArgs ra{};
     ra.part_w = a.part_w, ra.part_next = dxn ? a.part_next : nullptr, ra.part_gate = gate ? a.part_gate : nullptr;
