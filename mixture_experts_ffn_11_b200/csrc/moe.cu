@@ -1714,9 +1714,11 @@ moe_status_t moe_fp8_row_quantize(const moe_bf16_t* x, const int32_t* row_src, i
     DeviceInfo di;
     moe_status_t st = device_info(di);
     if (st != MOE_OK) return st;
-    const long items = (long)R * ((K / 8 + F8_CHUNK_VEC - 1) / F8_CHUNK_VEC);
+    const int chunks = (K / 8 + F8_CHUNK_VEC - 1) / F8_CHUNK_VEC;
+    if (chunks > 65535) return fail(MOE_ERR_INVALID_ARG, "K=%d too large", K);
+    const int grid = grid_cap(((long)R + 7) / 8, std::max(1, di.sms / chunks), 6);
     return check_launch("fp8_row_quantize",
-                        launch_pdl(fp8_row_quantize_kernel, dim3(grid_cap((items + 7) / 8, di.sms, 8)), dim3(256), 0, stream,
+                        launch_pdl(fp8_row_quantize_kernel, dim3(grid, chunks), dim3(256), 0, stream,
                                    reinterpret_cast<const __nv_bfloat16*>(x), row_src, T, K, R, q, s));
 }
 
