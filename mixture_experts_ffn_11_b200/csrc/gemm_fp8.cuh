@@ -11,8 +11,8 @@
 // Roles (384 threads per CTA, both CTAs):
 //   warp 0      TMA producer: per 128-wide K block (one ring stage) this CTA's 128 weight rows (one box) and its half of the
 //               token rows (one box); completion is counted on the leader's full[stage].
-//   warp 1      TMEM allocation; in the leader the MMA issuer: per K block four MMAs (K = 32 each) per token group into its next
-//               TMEM buffer, so the tensor cores run ahead of the warps that read them.
+//   warp 1      TMEM allocation; in the leader the MMA issuer: per K block four MMAs (K = 32 each) into the next of NBUF
+//               TMEM buffers, so the tensor cores run ahead of the warps that read them.
 //   warps 2, 3  scales: sa of the tile's tokens and sw of this CTA's weight rows into a ring by asynchronous copies (warp 2),
 //               their products into another (warp 3). (Loaded through registers two K blocks ahead, the loads' latency set the
 //               pace: 1.2 us per K block at any tile size.)
@@ -51,24 +51,12 @@ struct Gemm8Shape {
     static constexpr int W_BYTES = 128 * F8_BLOCK;
     static constexpr int X_BYTES = MAXN / 2 * F8_BLOCK;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr int STAGES = MAXN == 256 ? 5 : 8;
-    // A tile of up to 256 tokens is two MMAs per K step, one for each warpgroup's tokens, into two buffers of 128 columns
-    // each: a buffer's way from MMA to free again (commit, read, arrive across the pair) is about 1300 cycles besides the
-    // MMAs, which two 256-column buffers shared by the warpgroups hid less of (prompt products 0.66 ms).
-    static constexpr bool SPLIT = MAXN == 256;
-    static constexpr int GROUPS = SPLIT ? 2 : 1;          // MMAs (token groups) per K step
-    static constexpr int BUF_COLS = MAXN / GROUPS;        // TMEM columns of a buffer
-    static constexpr int NBUF = 512 / MAXN;               // buffers per group
+    static constexpr int STAGES = MAXN == 256 ? 5 : (MAXN == 128 ? 7 : 8);
+    static constexpr int NBUF = 512 / MAXN;
     static constexpr int TILE_W = GATEUP ? 128 : 256;
     static constexpr int SCALE_BYTES = (GATEUP ? 2 : 1) * MAXN * 4;
     static constexpr int RAW_FLOATS = MAXN + 4;
     static constexpr int EPI_BYTES = 8 * 2 * 2048;  // two staging blocks per warp
-    // tokens of the first (or only) MMA and of the second, for `rows` token rows: multiples of 32
-    __device__ static __forceinline__ int group_tokens(int rows, int group) {
-        const int n = (rows + 31) / 32;
-        if (!SPLIT) return 32 * n;
-        return 32 * (group == 0 ? (n + 1) / 2 : n / 2);
-    }
     static constexpr int BAR_BYTES = 512;
     static constexpr int TABLE_BYTES = (2 * (GG_MAX_GROUPS + 1) * 4 + 127) / 128 * 128;
     static constexpr int SMEM_BYTES =
@@ -76,7 +64,7 @@ struct Gemm8Shape {
         G8_RAW_STAGES * RAW_FLOATS * 4 + BAR_BYTES + TABLE_BYTES;
     static_assert(STAGE_BYTES % 1024 == 0, "stage bases stay 1024-byte aligned");
     static_assert(SMEM_BYTES <= 232448, "shared memory");
-    static_assert((2 * STAGES + 2 * NBUF * GROUPS + 2 * G8_SCALE_STAGES + 2 * G8_RAW_STAGES + 2) * 8 + 8 <= BAR_BYTES, "barrier area");
+    static_assert((2 * STAGES + 2 * NBUF + 2 * G8_SCALE_STAGES + 2 * G8_RAW_STAGES + 2) * 8 + 8 <= BAR_BYTES, "barrier area");
 };
 
 // token boxes of 128, 64, 32, 16 rows
@@ -193,9 +181,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
     float* raw = reinterpret_cast<float*>(scales + G8_SCALE_STAGES * S::SCALE_BYTES);
     uint64_t* full_bar = reinterpret_cast<uint64_t*>(raw + G8_RAW_STAGES * S::RAW_FLOATS);  // used in the leader
     uint64_t* empty_bar = full_bar + STAGES;
-    uint64_t* tfull_bar = empty_bar + STAGES;             // [GROUPS][NBUF]
-    uint64_t* tempty_bar = tfull_bar + S::GROUPS * NBUF;  // [GROUPS][NBUF], used in the leader
-    uint64_t* sfull_bar = tempty_bar + S::GROUPS * NBUF;  // [G8_SCALE_STAGES]
+    uint64_t* tfull_bar = empty_bar + STAGES;  // [NBUF]
+    uint64_t* tempty_bar = tfull_bar + NBUF;   // [NBUF], used in the leader
+    uint64_t* sfull_bar = tempty_bar + NBUF;   // [G8_SCALE_STAGES]
     uint64_t* sempty_bar = sfull_bar + G8_SCALE_STAGES;
     uint64_t* rfull_bar = sempty_bar + G8_SCALE_STAGES;  // [G8_RAW_STAGES]
     uint64_t* rempty_bar = rfull_bar + G8_RAW_STAGES;
@@ -219,9 +207,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
-        for (int b = 0; b < S::GROUPS * NBUF; ++b) {
+        for (int b = 0; b < NBUF; ++b) {
             mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], 16 / S::GROUPS);  // the warps that read the buffer, of both CTAs
+            mbar_init(&tempty_bar[b], 16);  // the warps that read it, of both CTAs
         }
         for (int s = 0; s < G8_SCALE_STAGES; ++s) {
             mbar_init(&sfull_bar[s], 32);
@@ -317,11 +305,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             for (int tile = cluster; tile < total && ok; tile += n_clusters) {
                 int g, wb, r0, rows;
                 locate(tile, g, wb, r0, rows);
-                // this CTA's half of each group's tokens, in the smallest box that holds it
-                const int n0 = S::group_tokens(rows, 0), n1 = S::SPLIT ? S::group_tokens(rows, 1) : 0;
-                const int b0 = swap_box_index(n0 / 2), b1 = swap_box_index(n1 / 2);
-                const int x0 = r0 + (int)rank * (n0 / 2), x1 = r0 + n0 + (int)rank * (n1 / 2);
-                const uint32_t tx = 2u * (uint32_t)(S::W_BYTES + ((128 >> b0) + (n1 > 0 ? 128 >> b1 : 0)) * F8_BLOCK);
+                const int half = (rows + 31) / 32 * 16;  // token rows per CTA (N / 2), in the smallest box that holds them
+                const int bi = swap_box_index(half);
+                const int xrow0 = r0 + (int)rank * half;
+                const uint32_t tx = 2u * (uint32_t)(S::W_BYTES + (128 >> bi) * F8_BLOCK);
                 for (int kb = 0; kb < KB; ++kb) {
                     if (lane == 0) {
                         ok = mbar_wait_within(&empty_bar[stage], phase ^ 1u, abort_flag, limit);
@@ -333,9 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                                 tma_load_5d_pair(sw, &tmW, bar, kb * F8_BLOCK, 0, 0, wb * 8 + 4 * (int)rank, g, pol_w);
                             else
                                 tma_load_3d_pair(sw, &tmW, bar, kb * F8_BLOCK, wb * 256 + 128 * (int)rank, g, pol_w);
-                            tma_load_2d_pair(sw + S::W_BYTES, &tmX.x[b0], bar, kb * F8_BLOCK, x0, pol_x);
-                            if (S::SPLIT && n1 > 0)
-                                tma_load_2d_pair(sw + S::W_BYTES + S::X_BYTES / 2, &tmX.x[b1], bar, kb * F8_BLOCK, x1, pol_x);
+                            tma_load_2d_pair(sw + S::W_BYTES, &tmX.x[bi], bar, kb * F8_BLOCK, xrow0, pol_x);
                         }
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -359,59 +344,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             // loop, so that descriptors and addresses stay in uniform registers, and the next K block's barriers are polled
             // between this one's MMAs and commits.
             if (leader) {
-                int stage = 0;
-                uint32_t phase = 0;
-                int buf[S::GROUPS] = {};
-                uint32_t buf_phase[S::GROUPS] = {};
+                int stage = 0, buf = 0;
+                uint32_t phase = 0, buf_phase = 0;
                 const bool elected = elect_one();
                 bool ok = __all_sync(0xffffffffu, test_stall(never_bar, abort_flag));
-                bool ready = false;  // the stage and the first group's buffer of the coming K block were seen complete
+                bool ready = false;  // the coming K block's barriers were seen complete
                 for (int tile = cluster; tile < total && ok; tile += n_clusters) {
                     int g, wb, r0, rows;
                     locate(tile, g, wb, r0, rows);
+                    const uint32_t idesc = idesc_e4m3_f32(256, (rows + 31) / 32 * 32);
                     for (int kb = 0; kb < KB; ++kb) {
                         if (!ready) {
-                            ok = mbar_wait_within(&tempty_bar[buf[0]], buf_phase[0] ^ 1u, abort_flag, limit) &&
+                            ok = mbar_wait_within(&tempty_bar[buf], buf_phase ^ 1u, abort_flag, limit) &&
                                  mbar_wait_within(&full_bar[stage], phase, abort_flag, limit);
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
                         }
                         tc_fence_after_sync();
                         const uint32_t sa = smem_u32(stages + stage * S::STAGE_BYTES);
-                        const uint64_t wdesc = smem_desc_sw128(sa);
-#pragma unroll
-                        for (int gr = 0; gr < S::GROUPS; ++gr) {
-                            const int n = S::group_tokens(rows, gr);
-                            if (n == 0) continue;
-                            uint64_t* const tempty = &tempty_bar[gr * NBUF + buf[gr]];
-                            if (gr > 0 && !__all_sync(0xffffffffu, mbar_test_wait(smem_u32(tempty), buf_phase[gr] ^ 1u))) {
-                                ok = __all_sync(0xffffffffu, mbar_wait_within(tempty, buf_phase[gr] ^ 1u, abort_flag, limit));
-                                if (!ok) break;
-                                tc_fence_after_sync();
-                            }
-                            const uint64_t xdesc = smem_desc_sw128(sa + S::W_BYTES + gr * (S::X_BYTES / 2));
-                            const uint32_t d_tmem = tmem_base + (uint32_t)((gr * NBUF + buf[gr]) * S::BUF_COLS);
-                            const uint32_t idesc = idesc_e4m3_f32(256, n);
-                            if (elected) {
-#pragma unroll
-                                for (int k = 0; k < F8_BLOCK / 32; ++k)
-                                    umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
-                                umma_commit_pair_multicast(&tfull_bar[gr * NBUF + buf[gr]], 0x3);
-                            }
-                            if (++buf[gr] == NBUF) {
-                                buf[gr] = 0;
-                                buf_phase[gr] ^= 1u;
-                            }
-                        }
-                        if (!ok) break;
+                        const uint64_t wdesc = smem_desc_sw128(sa), xdesc = smem_desc_sw128(sa + S::W_BYTES);
+                        const uint32_t d_tmem = tmem_base + (uint32_t)(buf * MAXN);
+                        uint64_t* const tfull = &tfull_bar[buf];
                         uint64_t* const empty = &empty_bar[stage];
+                        if (elected) {
+#pragma unroll
+                            for (int k = 0; k < F8_BLOCK / 32; ++k)
+                                umma_e4m3_ss_pair(d_tmem, wdesc + 2 * k, xdesc + 2 * k, idesc, k != 0 ? 1u : 0u);
+                        }
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
-                        const bool te = mbar_test_wait(smem_u32(&tempty_bar[buf[0]]), buf_phase[0] ^ 1u);
+                        if (++buf == NBUF) {
+                            buf = 0;
+                            buf_phase ^= 1u;
+                        }
+                        const bool te = mbar_test_wait(smem_u32(&tempty_bar[buf]), buf_phase ^ 1u);
                         const bool fu = mbar_test_wait(smem_u32(&full_bar[stage]), phase);
-                        if (elected) umma_commit_pair_multicast(empty, 0x3);
+                        if (elected) {
+                            umma_commit_pair_multicast(tfull, 0x3);
+                            umma_commit_pair_multicast(empty, 0x3);
+                        }
                         ready = __all_sync(0xffffffffu, te && fu);
                     }
                 }
@@ -499,7 +472,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         if constexpr (MAXN == 256) more_registers<216>();
         constexpr int CHUNKS = MAXN / 32;  // 16-token chunks of this warpgroup's half
         const int q = warp & 3, hw = (warp - 4) >> 2;
-        const int gr = S::SPLIT ? hw : 0;
         const uint32_t tempty_leader = mapa_shared(smem_u32(tempty_bar), 0);
         bool ready = false;  // the coming K block's sums and scales were seen complete
         uint8_t* stage_base = epi + (warp - 4) * 4096;
@@ -509,10 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         for (int tile = cluster; tile < total && ok; tile += n_clusters) {
             int g, wb, r0, rows;
             locate(tile, g, wb, r0, rows);
-            // this warpgroup's tokens: its own group, or half of the only one (from tile row first, in TMEM column col)
-            const int nh = S::SPLIT ? S::group_tokens(rows, gr) : S::group_tokens(rows, 0) / 2;
-            const int first = S::SPLIT ? hw * S::group_tokens(rows, 0) : hw * nh;
-            const int col = S::SPLIT ? 0 : first;
+            const int nh = (rows + 31) / 32 * 16, first = hw * nh;  // this warpgroup's tokens
             float2 acc[CHUNKS][2][4];
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c)
@@ -526,17 +495,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!ready) {
                         ok = mbar_wait_within(&sfull_bar[slot], s_phase, abort_flag, limit) &&
-                             (NB == 0 || mbar_wait_within(&tfull_bar[gr * NBUF + buf], buf_phase, abort_flag, limit));
+                             mbar_wait_within(&tfull_bar[buf], buf_phase, abort_flag, limit);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t t0 =
-                        tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((gr * NBUF + buf) * S::BUF_COLS + col);
+                    const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAXN + first);
                     const float* sc = reinterpret_cast<const float*>(scales + slot * S::SCALE_BYTES) + first + 2 * (lane & 3);
-                    const uint32_t freed = tempty_leader + (uint32_t)((gr * NBUF + buf) * 8);
+                    const uint32_t freed = tempty_leader + (uint32_t)(buf * 8);
                     uint64_t* const s_freed = &sempty_bar[slot];
-                    if (NB > 0 && ++buf == NBUF) {
+                    if (++buf == NBUF) {
                         buf = 0;
                         buf_phase ^= 1u;
                     }
@@ -546,10 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                     }
                     bool next = false;
                     float v[2][2][16];
-                    if constexpr (NB > 0) {
-                        tmem_ld_16x32(t0, v[0][0]);
-                        tmem_ld_16x32(t0 + (16u << 16), v[0][1]);
-                    }
+                    tmem_ld_16x32(t0, v[0][0]);
+                    tmem_ld_16x32(t0 + (16u << 16), v[0][1]);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         float2 s0[4], s1[4];
@@ -570,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                                 mbar_arrive(s_freed);
                             }
                             next = mbar_test_wait(smem_u32(&sfull_bar[slot]), s_phase) &
-                                   mbar_test_wait(smem_u32(&tfull_bar[gr * NBUF + buf]), buf_phase);
+                                   mbar_test_wait(smem_u32(&tfull_bar[buf]), buf_phase);
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -581,23 +547,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                                 fma2_acc(acc[2 * b + (j >> 1)][1][2 * (j & 1) + i], v[b & 1][1][r], v[b & 1][1][r + 1], s1[j]);
                             }
                     }
-                    if constexpr (NB == 0) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(s_freed);
-                    }
                     ready = kb + 1 < KB && __all_sync(0xffffffffu, next);
                 }
             };
             if constexpr (MAXN == 64) {
                 mainloop(std::integral_constant<int, 1>());
+            } else if (MAXN == 128 || nh <= 64) {
+                if (nh <= 32)
+                    mainloop(std::integral_constant<int, 1>());
+                else
+                    mainloop(std::integral_constant<int, 2>());
             } else {
-                switch (nh / 32) {
-                    case 0: mainloop(std::integral_constant<int, 0>()); break;  // (its only part is to free the scales)
-                    case 1: mainloop(std::integral_constant<int, 1>()); break;
-                    case 2: mainloop(std::integral_constant<int, 2>()); break;
-                    case 3: mainloop(std::integral_constant<int, 3>()); break;
-                    default: mainloop(std::integral_constant<int, 4>()); break;
-                }
+                if (nh <= 96)
+                    mainloop(std::integral_constant<int, 3>());
+                else
+                    mainloop(std::integral_constant<int, MAXN == 256 ? 4 : 2>());
             }
             if (!ok) break;
             const int row_first = r0 + first, row_end = min(r0 + rows, row_first + nh);

@@ -163,6 +163,8 @@ cudaError_t set_gemm_attributes() {
         e = cudaFuncSetAttribute(grouped_gemm_fp4_warp_kernel<false>, a, GemmFp4WarpShape<false>::MAX_SMEM);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<true, 256>, a, Gemm8Shape<true, 256>::SMEM_BYTES);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<false, 256>, a, Gemm8Shape<false, 256>::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<true, 128>, a, Gemm8Shape<true, 128>::SMEM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<false, 128>, a, Gemm8Shape<false, 128>::SMEM_BYTES);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<true, 64>, a, Gemm8Shape<true, 64>::SMEM_BYTES);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp8_kernel<false, 64>, a, Gemm8Shape<false, 64>::SMEM_BYTES);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(grouped_gemm_fp4_kernel<16, true>, a, GemmFp4Shape<16, true>::SMEM_BYTES);
@@ -909,6 +911,7 @@ moe_status_t gemm_fp8(const uint8_t* a, const float* sa, const uint8_t* w, const
     if (st != MOE_OK) return st;
     if (di.sms < 2) return fail(MOE_ERR_UNSUPPORTED, "the fp8 GEMM needs CTA pairs");
     if (M == 0) return MOE_OK;
+    if ((long)M <= 112L * G && (long)M > 48L * G) return launch_fp8<GATEUP, 128>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
     if ((long)M <= 48L * G) return launch_fp8<GATEUP, 64>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
     return launch_fp8<GATEUP, 256>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
 }
