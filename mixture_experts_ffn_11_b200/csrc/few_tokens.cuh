@@ -136,6 +136,85 @@ __device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
     return v;
 }
 
+// warp_route_select (route.cuh) for the logits of one token, the same choices and weights bit for bit, with the warp's arg-max by
+// two integer reductions instead of ten shuffles a round (every CTA waits for this). A NaN logit counts as the lowest:
+// comparisons with it would leave the warp without a common choice.
+__device__ __forceinline__ void few_route_select(const float* l, int E, int k, int mode, int32_t* idx_row, float* w_row) {
+    const int lane = threadIdx.x & 31;
+    const int per = (E + 31) / 32;
+    const auto get = [&](int e) {
+        const float v = __ldcg(l + e);
+        return v == v ? v : -INFINITY;
+    };
+    // unsigned keys in the order of the values (+0 and -0 alike), above 0, which stands for nothing left
+    const auto key_of = [](float v) {
+        const uint32_t u = __float_as_uint(v + 0.f);
+        return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    };
+    constexpr int RPER = 8;  // up to 256 experts stay in registers
+    uint32_t keys[RPER];
+    if (per <= RPER) {
+#pragma unroll
+        for (int s = 0; s < RPER; ++s) {
+            const int e = s * 32 + lane;
+            keys[s] = s < per && e < E ? key_of(get(e)) : 0u;
+        }
+    }
+    uint32_t taken = 0;
+    float my_v = 0.f;
+    int my_e = -1;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = 0u;
+        int best_s = 0;
+        if (per <= RPER) {
+#pragma unroll
+            for (int s = 0; s < RPER; ++s) {
+                const uint32_t c = (taken >> s) & 1u ? 0u : keys[s];
+                if (c > best) best = c, best_s = s;  // ascending ids: '>' keeps the lower one
+            }
+        } else {
+            for (int s = 0; s < per; ++s) {
+                const int e = s * 32 + lane;
+                const uint32_t c = e < E && !((taken >> s) & 1u) ? key_of(get(e)) : 0u;
+                if (c > best) best = c, best_s = s;
+            }
+        }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(best_s * 32 + lane) : 0xffffffffu);
+        if ((e & 31) == lane) taken |= 1u << (e >> 5);
+        if (lane == j) {
+            my_e = e;
+            my_v = __uint_as_float(top & 0x80000000u ? top ^ 0x80000000u : ~top);
+        }
+    }
+    const bool mine = lane < k;
+    const float vmax = __shfl_sync(0xffffffffu, my_v, 0);
+    float w = 0.f;
+    if (mode == MOE_ROUTE_SIGMOID_TOPK_NORM) {
+        const float s = mine ? 1.f / (1.f + expf(-my_v)) : 0.f;
+        w = s / warp_sum(s);
+    } else {
+        const float ex = mine ? expf(my_v - vmax) : 0.f;
+        const float zsel = warp_sum(ex);
+        if (mode == MOE_ROUTE_SOFTMAX_TOPK_RENORM) {
+            float part = 0.f;
+            for (int s = 0; s < per; ++s) {
+                const int e = s * 32 + lane;
+                if (e < E) part += expf(get(e) - vmax);
+            }
+            const float zall = warp_sum(part);
+            const float p = ex / zall;  // probability under the full softmax
+            w = p / warp_sum(p);
+        } else {
+            w = ex / zsel;
+        }
+    }
+    if (mine) {
+        idx_row[lane] = my_e;
+        w_row[lane] = w;
+    }
+}
+
 // Wait until all CTAs of the grid have arrived on *counter (zero at the start). False when the wait ran out.
 __device__ __forceinline__ bool grid_barrier(int* counter, int* s_flag) {
     __syncthreads();
@@ -184,16 +263,10 @@ __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs
     const int g = lane >> 2, t4 = lane & 3;
     const int T = p.T;
 
+    grid_dep_wait();  // the logits
+
     // ---- route ----
-    for (int t = warp; t < T; t += FT_WARPS) {
-        // a NaN logit counts as the lowest: comparisons with it would leave the warp without a common choice
-        const float* l = p.logits + (size_t)t * p.E;
-        const auto logit = [=](int e) {
-            const float v = l[e];
-            return v == v ? v : -INFINITY;
-        };
-        warp_route_select(logit, p.E, p.k, p.mode, s_idx + t * p.k, s_w + t * p.k);
-    }
+    for (int t = warp; t < T; t += FT_WARPS) few_route_select(p.logits + (size_t)t * p.E, p.E, p.k, p.mode, s_idx + t * p.k, s_w + t * p.k);
     for (int e = threadIdx.x; e < p.E; e += FT_THREADS) s_count[e] = 0;
     for (int i = threadIdx.x; i < (slots + 1) * 8 * NT; i += FT_THREADS) s_choice[i] = -1;
     for (int i = threadIdx.x; i <= slots; i += FT_THREADS) s_tiles[i] = 0;
@@ -210,25 +283,28 @@ __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs
         }
     }
     __syncthreads();
-    if (warp == 0) {  // the active experts in ascending order
+    if (warp == 0) {  // the active experts, in the order in which the slots name them first
         int n = 0, rows = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int c = e0 + lane < p.E ? s_count[e0 + lane] : 0;
-            const unsigned m = __ballot_sync(0xffffffffu, c > 0);
-            int before = c;
+        for (int s0 = 0; s0 < slots; s0 += 32) {
+            const int s = s0 + lane;
+            const bool first = s < slots && s_rank[s] == 0;
+            const int e = first ? s_idx[s] : 0;
+            const int c = first ? s_count[e] : 0;
+            const unsigned m = __ballot_sync(0xffffffffu, first);
+            int upto = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, before, o);
-                if (lane >= o) before += v;
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
             }
-            if (c > 0) {
+            if (first) {
                 const int at = n + __popc(m & lanemask_lt());
-                s_active[at] = e0 + lane;
-                s_place[e0 + lane] = at;
-                s_first[at] = rows + before - c;
+                s_active[at] = e;
+                s_place[e] = at;
+                s_first[at] = rows + upto - c;
             }
             n += __popc(m);
-            rows += __shfl_sync(0xffffffffu, before, 31);
+            rows += __shfl_sync(0xffffffffu, upto, 31);
         }
         if (lane == 0) {
             s_first[n] = rows;

@@ -834,11 +834,13 @@ cudaError_t launch_few(const FewArgs& a, int grid, cudaStream_t stream) {
     cfg.blockDim = dim3(FT_THREADS);
     cfg.dynamicSmemBytes = few_smem<NT>(a.T * a.k, a.E);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_pdl
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, few_tokens_kernel<NT>, a);
 }
 
