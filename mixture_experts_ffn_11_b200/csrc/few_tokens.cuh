@@ -37,10 +37,16 @@ constexpr int FT_WARPS = 16;
 constexpr int FT_THREADS = FT_WARPS * 32;
 constexpr int FT_MAX_CTAS = 148;
 constexpr int FT_KC = 32;     // k values of a step: 64 bytes of a weight row
+// Ring of STAGES steps of (4 + NT) x 8 KB, and a buffer for the warps' sums, RB 16-row blocks of NT x 8 KB at a time. What is left
+// of the SM's 227 KB holds the tables. (25 to 32 tokens: the MMAs bound it, 16 per 2 KB of weights; three stages with a smaller
+// buffer for the sums measured the same as two.)
 template <int NT>
-constexpr int FT_STAGES = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // ring of steps, (4 + NT) x 8 KB each
-template <int NT>
-constexpr int FT_RED_BLOCKS = NT == 4 ? 1 : 2;  // 16-row blocks whose sums the reduction buffer holds at a time, NT x 8 KB each
+struct FewShape {
+    static constexpr int STAGES = NT == 1 ? 4 : (NT == 4 ? 2 : 3);
+    static constexpr int RB = NT <= 2 ? 2 : 1;
+    static constexpr int RING_BYTES = STAGES * (4 + NT) * FT_WARPS * 32 * 16;
+    static constexpr int RED_BYTES = FT_WARPS * RB * NT * 32 * 16;
+};
 constexpr int FT_LOGIT_THREADS = 256;
 
 // ---- logits: one CTA per expert, fp32, 8 tokens at a time; also clears the counters of the kernel behind it ----
@@ -242,11 +248,11 @@ __device__ __forceinline__ bool grid_barrier(int* counter, int* s_flag) {
 template <int NT>
 __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr int STAGES = FT_STAGES<NT>, SLOT_BYTES = FT_THREADS * 16, STAGE_BYTES = (4 + NT) * SLOT_BYTES;
+    using S = FewShape<NT>;
+    constexpr int STAGES = S::STAGES, RB = S::RB, SLOT_BYTES = FT_THREADS * 16, STAGE_BYTES = (4 + NT) * SLOT_BYTES;
     const uint32_t ring = smem_u32(smem_raw) + threadIdx.x * 16;  // this thread's 16 bytes of slot 0, stage 0
-    float4* red = reinterpret_cast<float4*>(smem_raw + STAGES * STAGE_BYTES);  // [warp][RB][NT][lane]
-    constexpr int RB = FT_RED_BLOCKS<NT>;
-    int* words = reinterpret_cast<int*>(red + FT_WARPS * RB * NT * 32);
+    float4* red = reinterpret_cast<float4*>(smem_raw + S::RING_BYTES);  // [warp][RB][NT][lane]
+    int* words = reinterpret_cast<int*>(smem_raw + S::RING_BYTES + S::RED_BYTES);
     const int slots = p.T * p.k;
     int* s_idx = words;
     float* s_w = reinterpret_cast<float*>(s_idx + slots);
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs
             }
         }
     };
-    auto publish = [&](int tiles, int m0) {  // this warp's sums of blocks m0 .. m0 + RB - 1, for the CTA to add
+    auto publish = [&](int tiles, int m0) {  // this warp's sums of RB blocks from m0, for the CTA to add
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -442,8 +448,8 @@ __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs
                 __syncthreads();
                 for (int i = threadIdx.x; i < 64 * RB * used; i += FT_THREADS) {
                     const int n = i / (64 * RB), m = (i >> 6) % RB, j = (i >> 3) & 7, col = i & 7;
-                    const int j0 = (u - (routed ? a : A) * fb) * 16 + (m0 + m) * 8 + j;
-                    if (n * 8 + col >= count || j0 >= (routed ? p.f : p.fs)) continue;
+                    const int j0 = (u - (routed ? a : A) * fb) * 16 + (m0 + m) * 8 + j, at = n * 8 + col;
+                    if (at >= count || j0 >= (routed ? p.f : p.fs)) continue;
                     float gate = 0.f, upv = 0.f;
 #pragma unroll
                     for (int q = 0; q < FT_WARPS; ++q) {
@@ -451,9 +457,9 @@ __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs
                         upv += element(q, m, n, j + 8, col);
                     }
                     float h = swiglu(gate, upv);
-                    int s = slots + n * 8 + col;
+                    int s = slots + at;
                     if (routed) {
-                        s = s_rows[s_first[a] + n * 8 + col];
+                        s = s_rows[s_first[a] + at];
                         h *= s_w[s];
                     }
                     p.h[(size_t)s * p.ldh + j0] = __float2bfloat16_rn(h);
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs
                     else
                         mine[t * 32 + c] = v;
                 }
-                if (m0 + RB < 2) __syncthreads();
+                __syncthreads();
             }
             if (!whole) {  // cut between CTAs: the last one to arrive adds the parts in their order
                 const long x0 = (long)cb * per, x1 = x0 + per - 1;

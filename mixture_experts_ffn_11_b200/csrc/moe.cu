@@ -812,17 +812,21 @@ FewWorkspace few_workspace(int T, int d, int f, int fs, int k) {
     return w;
 }
 
+constexpr size_t kFewMaxSmem = 232448;
+
 template <int NT>
 size_t few_smem(int slots, int E) {
-    return (size_t)FT_STAGES<NT> * (4 + NT) * FT_THREADS * 16 + (size_t)FT_WARPS * FT_RED_BLOCKS<NT> * NT * 32 * 16 +
-           (size_t)FewTables::words(slots, E) * 4 + (size_t)(slots + 1) * 8 * NT;
+    using S = FewShape<NT>;
+    return (size_t)S::RING_BYTES + S::RED_BYTES + (size_t)FewTables::words(slots, E) * 4 + (size_t)(slots + 1) * 8 * NT;
 }
 
 cudaError_t set_few_attributes() {
     const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(few_tokens_kernel<1>, a, (int)few_smem<1>(8 * 32, 1024));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(few_tokens_kernel<2>, a, (int)few_smem<2>(16 * 32, 1024));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(few_tokens_kernel<4>, a, (int)few_smem<4>(FT_MAX_T * 32, 1024));
+    const int most = (int)kFewMaxSmem;
+    cudaError_t e = cudaFuncSetAttribute(few_tokens_kernel<1>, a, most);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(few_tokens_kernel<2>, a, most);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(few_tokens_kernel<3>, a, most);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(few_tokens_kernel<4>, a, most);
     return e;
 }
 
@@ -1679,10 +1683,13 @@ moe_status_t moe_few_tokens(const moe_bf16_t* x, const float* w_router, const fl
     // at least one step of the down projection per CTA (some expert is always active)
     const long steps = (long)((f + FT_KC - 1) / FT_KC) * ((d + 31) / 32);
     const int grid = (int)std::min<long>(steps, std::min(di.sms, FT_MAX_CTAS));
+    // the smallest number of 8-token blocks; three of them only where the tables (many choices, many experts) fit beside its ring
     if (T <= 8)
         e = launch_few<1>(a, grid, stream);
     else if (T <= 16)
         e = launch_few<2>(a, grid, stream);
+    else if (T <= 24 && few_smem<3>(T * k, E) <= kFewMaxSmem)
+        e = launch_few<3>(a, grid, stream);
     else
         e = launch_few<4>(a, grid, stream);
     return check_launch("few_tokens", e);

@@ -68,8 +68,9 @@ class MoEFFN:
     pass then gathers x_perm itself. Off by default: on B200 the separate gather and combine kernels are faster
     (the per-row gather loads and the combine's arrival counting slow the GEMMs by more than the two kernels
     take).
-    few: with bf16 weights and 1 to 32 tokens, run the whole layer in two kernels (moe_few_tokens) instead of eight. Results
-    agree to rounding, not bit for bit (the routing weight is applied before h is rounded, and the experts' outputs are
+    few: with bf16 weights and 1 to 16 tokens, run the whole layer in two kernels (moe_few_tokens) instead of eight (measured faster
+    there on every shape: 50 against 128 us for one token on 4 of 32 experts of 2880 x 2880, 258 against 267 for 16; at 20 to 32
+    tokens, which the kernels also take, the grouped GEMMs are up to 1.5 times as fast on some shapes). Results agree to rounding, not bit for bit (the routing weight is applied before h is rounded, and the experts' outputs are
     summed without rounding). Not used by a training forward, whose backward pass reads the separate calls' buffers.
     """
 
@@ -309,7 +310,7 @@ class MoEFFN:
 
     def _few(self, T: int) -> bool:
         """Whether forward() runs the whole layer in the few-token kernels for T tokens."""
-        return self.few and self.weights == "bf16" and 0 < T <= N.FEW_TOKENS_MAX
+        return self.few and self.weights == "bf16" and 0 < T <= 16
 
     def _fold(self, T: int) -> bool:
         """Whether forward() computes the shared expert inside the routed MXFP4 GEMMs for T tokens: when the
