@@ -540,7 +540,9 @@ moe_status_t moe_router_backward(const moe_bf16_t* x, const float* w_router, con
  * length of a sequence a row per sequence. Gains w are fp32 [d], the gate bf16.
  * Sums are in fp32; out and xn are rounded once. d: a positive multiple of 8,
  * at most 16384. T = 0 launches nothing (the backward calls then zero dw and
- * dw_next). Rows that hold infinities or NaN give NaN in those rows only. */
+ * dw_next). A row that holds an infinity or NaN gives NaN in that row only
+ * (and in the gradients summed over rows); so does a row of zeros with
+ * eps = 0. */
 typedef enum { MOE_STREAM_BF16 = 0, MOE_STREAM_FP32 = 1 } moe_stream_type_t;
 
 /* xn [T][d] bf16 and rstd [T] fp32 of x [T][d] (type `type`). eps >= 0. */
@@ -615,8 +617,9 @@ moe_status_t moe_set_gemm_kernel(moe_gemm_kernel_t kind);
  * in flight are waited for (each wait bounded again), tensor memory is freed
  * and the kernel returns; the CUDA context stays usable. This call sets, on
  * the current device, the wait limit in nanoseconds (0 restores the default
- * of 2 s) and, with stall != 0, makes the MMA-issuing warp of every bf16
- * grouped GEMM first wait on a barrier that nothing arrives on, so that a
+ * of 2 s) and, with stall != 0, makes the MMA-issuing warp of every bf16 and
+ * e4m3 grouped GEMM first wait on a barrier that nothing arrives on, and the
+ * barrier inside moe_few_tokens wait for one arrival too many, so that a
  * test can run the timeout path on purpose. It synchronises the device first.
  * Results of GEMMs launched while stall is set are undefined; the device
  * error word reports the timeout. Not for normal use. */

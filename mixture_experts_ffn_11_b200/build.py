@@ -5,7 +5,7 @@
 Run it by path (or load it with load_build_module below): importing the package itself loads libmoe.so,
 which is what this script produces.
 
-The library is one translation unit (csrc/moe.cu plus the kernel headers it includes) compiled by nvcc
+The library is one translation unit (csrc/operators.cu, which includes csrc/moe.cu and the kernel headers) compiled by nvcc
 into a shared object next to this file, so it travels with the source tree.
 """
 from __future__ import annotations
@@ -29,7 +29,7 @@ def sources():
 
 def nvcc_command(out: str = LIB, verbose: bool = False, extra=()):
     cmd = ["nvcc", "-O3", "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-lineinfo", *ARCH,
-           "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "moe.cu"), "-o", out, *extra]
+           "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "operators.cu"), "-o", out, *extra]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     return cmd

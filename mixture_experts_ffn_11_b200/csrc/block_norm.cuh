@@ -15,6 +15,7 @@
 // the copies' extra latency.
 #pragma once
 #include "common.cuh"
+#include "sync.cuh"
 
 namespace moe {
 

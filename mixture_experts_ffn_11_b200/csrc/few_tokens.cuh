@@ -29,6 +29,7 @@
 #include "common.cuh"
 #include "gemm.cuh"
 #include "route.cuh"
+#include "sync.cuh"
 
 namespace moe {
 
@@ -228,10 +229,12 @@ __device__ __forceinline__ bool grid_barrier(int* counter, int* s_flag) {
         __threadfence();
         atomicAdd(counter, 1);
         const uint64_t t0 = globaltimer_ns(), limit = wait_limit_ns();
+        // (the test hook moe_test_set_wait: one arrival more than there are)
+        const int want = (int)gridDim.x + (*reinterpret_cast<volatile int*>(&g_wait_stall) != 0 ? 1 : 0);
         int ok = 1, seen;
         for (;;) {
             asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(counter) : "memory");
-            if (seen >= (int)gridDim.x) break;
+            if (seen >= want) break;
             if (globaltimer_ns() - t0 > limit) {
                 flag_error(MOE_DEVERR_WAIT_TIMEOUT);
                 ok = 0;

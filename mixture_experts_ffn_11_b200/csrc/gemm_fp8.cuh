@@ -31,6 +31,7 @@
 #include "fp8_quant.cuh"
 #include "gemm.cuh"
 #include "gemm_swap.cuh"
+#include "sync.cuh"
 
 namespace moe {
 

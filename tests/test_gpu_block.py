@@ -40,7 +40,8 @@ def weights(E, d, f, fs=0, seed=0):
 
 
 def off(a, b):
-    return float((a.double() - b.double()).norm() / b.double().norm())
+    a, b = a.detach().double(), b.detach().double()
+    return float((a - b).norm() / b.norm())
 
 
 @pytest.mark.parametrize("T,fs", [(1, 0), (5, 160), (300, 0), (1000, 96)])
