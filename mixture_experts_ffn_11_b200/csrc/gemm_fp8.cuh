@@ -455,9 +455,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                         const float b0 = from[MAXN], b1 = from[MAXN + 1];
 #pragma unroll
                         for (int i = 0; i < PER; ++i) {
-                            const float a = from[lane + 32 * i];
-                            to[lane + 32 * i] = a * b0;
-                            if constexpr (GATEUP) to[MAXN + lane + 32 * i] = a * b1;
+                            // gate|up: the gate's products of two tokens, then the up rows', so that one load brings all four
+                            const int t = lane + 32 * i;
+                            const float a = from[t];
+                            if constexpr (GATEUP) {
+                                to[4 * (t >> 1) + (t & 1)] = a * b0;
+                                to[4 * (t >> 1) + 2 + (t & 1)] = a * b1;
+                            } else {
+                                to[t] = a * b0;
+                            }
                         }
                         mbar_arrive(r_freed);
                         mbar_arrive(filled);
@@ -502,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                     }
                     tc_fence_after_sync();
                     const uint32_t t0 = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * MAXN + first);
-                    const float* sc = reinterpret_cast<const float*>(scales + slot * S::SCALE_BYTES) + first + 2 * (lane & 3);
+                    const float* sc = reinterpret_cast<const float*>(scales + slot * S::SCALE_BYTES) + (GATEUP ? 2 : 1) * (first + 2 * (lane & 3));
                     const uint32_t freed = tempty_leader + (uint32_t)(buf * 8);
                     uint64_t* const s_freed = &sempty_bar[slot];
                     if (++buf == NBUF) {
@@ -522,8 +528,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                         float2 s0[4], s1[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            s0[j] = *reinterpret_cast<const float2*>(sc + 32 * b + 8 * j);
-                            s1[j] = GATEUP ? *reinterpret_cast<const float2*>(sc + MAXN + 32 * b + 8 * j) : s0[j];
+                            if constexpr (GATEUP) {
+                                const float4 both = *reinterpret_cast<const float4*>(sc + 64 * b + 16 * j);
+                                s0[j] = make_float2(both.x, both.y);
+                                s1[j] = make_float2(both.z, both.w);
+                            } else {
+                                s0[j] = s1[j] = *reinterpret_cast<const float2*>(sc + 32 * b + 8 * j);
+                            }
                         }
                         tmem_wait_ld(v[b & 1][0], v[b & 1][1]);
                         if (b + 1 < NB) {
