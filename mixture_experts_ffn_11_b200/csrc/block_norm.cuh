@@ -618,8 +618,9 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
 }
 
 // Adds up what the CTAs left: blockIdx.y = 0: dw, 1: dw_next (with part_next), then the gate rows that lie in several CTAs, each by
-// the first CTA whose last row is one of its tokens but not the last (edge: that CTA). 32 columns per block; warp i adds the
-// partial rows i, i + 16, ..., then warp 0 adds the sixteen sums in order.
+// the first CTA whose last row is one of its tokens but not the last (edge: that CTA). 32 columns per block; 8 lanes cover them
+// with 16-byte loads, so a warp adds four partial rows at a time (warp i: rows 4i .. 4i + 3, then 64 further on), all in a fixed
+// order: the rows of a lane, the four lanes of a column, the sixteen warps.
 struct NormReduceArgs {
     const float *part_w, *part_next, *part_gate;
     float *dw, *dw_next, *dgate;
@@ -630,7 +631,7 @@ struct NormReduceArgs {
 constexpr int BNR_WARPS = 16;
 
 __global__ void __launch_bounds__(BNR_WARPS * 32) block_norm_reduce_kernel(const __grid_constant__ NormReduceArgs a) {
-    __shared__ float sums[BNR_WARPS][32];
+    __shared__ __align__(16) float sums[BNR_WARPS][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * 32 + lane;
     const int job = blockIdx.y;
@@ -649,12 +650,23 @@ __global__ void __launch_bounds__(BNR_WARPS * 32) block_norm_reduce_kernel(const
         to = a.dgate + group * a.d;
         pitch *= 2;
     }
-    float s = 0.f;
-    if (col < a.d) {
-#pragma unroll 8
-        for (int b = b0 + warp; b < b1; b += BNR_WARPS) s += from[b * pitch + (b == b0 ? (size_t)slot0 * a.d : 0) + col];
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int col4 = blockIdx.x * 32 + (lane & 7) * 4;
+    if (col4 < a.d) {
+#pragma unroll 5
+        for (int b = b0 + warp * 4 + (lane >> 3); b < b1; b += BNR_WARPS * 4) {
+            const float4 v = *reinterpret_cast<const float4*>(from + b * pitch + (b == b0 ? (size_t)slot0 * a.d : 0) + col4);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
     }
-    sums[warp][lane] = s;
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+        s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+        s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+    }
+    if (lane < 8) *reinterpret_cast<float4*>(&sums[warp][lane * 4]) = s;
     __syncthreads();
     if (warp == 0 && col < a.d) {
         float all = sums[0][lane];
