@@ -13,6 +13,12 @@
 // Many rows: they arrive in shared memory by bulk copies that run BN stages ahead (RowRing), so HBM does not wait for a row's
 // reductions; a stage is refilled as soon as the CTA has its row in registers. Few rows (at most one per CTA): plain loads, without
 // the copies' extra latency.
+//
+// Measured (HBM's floor at a copy's rate in brackets): behind the block with the next norm, 4096 rows of 2880 in bf16, 24.7 us
+// (14.4; its output mostly stays in L2, a row's reductions and stores set the pace); its gradient, 8192 rows of 4096 with an fp32 stream and
+// a gate, 103-118 us (92); the gradient in front, 4096 rows of 2880, 25.7-30 us (14.4), in two kernels, the second adding the
+// CTAs' partial sums in a fixed order (four rows of them at a time; one at a time 28.7 us in all); in front, 64 rows of 7168, 1.9 us (0.3),
+// a launch. Rows by plain loads, a barrier between rows: 28.9, 238, 42.3.
 #pragma once
 #include "common.cuh"
 #include "sync.cuh"

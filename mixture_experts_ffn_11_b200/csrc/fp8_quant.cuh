@@ -7,6 +7,8 @@
 // exactly computed remainder (a - q0 m, one fma) is within an ulp of a / m and is a / m itself where that is a fp32 number, so
 // the rounding to e4m3 comes out as that of the exact quotient. (Residual correction: Markstein, "Computation of elementary
 // functions on the IBM RISC System/6000 processor", 1990.)
+// HBM bounds both encoders: 16384 rows of 2880, 29 us (94 MB read, 47 MB written: 22 us at a copy's rate); the same number of rows
+// gathered from 4096, which stay in L2, 23 us (11).
 #pragma once
 #include <cuda_fp8.h>
 

@@ -128,7 +128,13 @@ moe_status_t launch_fp8(const uint8_t* a, const float* sa, const uint8_t* w, con
     return check_launch(GATEUP ? "grouped_gemm_gateup_fp8" : "grouped_gemm_down_fp8", e);
 }
 
-// Arguments of both products, then the launch: tiles of up to 256 token rows, or of 64 when the groups average at most 48.
+// Arguments of both products, then the launch. A tile covers up to 64, 128 or 256 token rows of a group: narrow tiles leave room for
+// more ring stages, wide ones read a group's weights fewer times. Which is decided by the average rows per group, the only
+// thing the host knows of the groups. Measured, groups within half of the average either way, gate|up / down in us:
+//   32 groups, d = f = 2880       average 32: 64 rows 87 / 52, 128 rows 88 / 53      48: 64 rows 108 / 60, 128 rows 94 / 54
+//                                 average 112: 128 rows 136 / 70, 256 rows 143 / 83  128: 128 rows 153 / 79, 256 rows 146 / 78
+//   128 groups, d 2048, f 768     average 96: 128 rows 104 / 68, 256 rows 117 / 71   128: 128 rows 123 / 80, 256 rows 126 / 75
+//   8 groups, d 4096, f 14336     average 96: 128 rows 193 / 92, 256 rows 220 / 112  128: 128 rows 275 / 133, 256 rows 245 / 118
 template <bool GATEUP>
 moe_status_t gemm_fp8(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, const int32_t* offsets, int G, int M,
                       int d, int f, moe_bf16_t* out, cudaStream_t stream) {
@@ -146,8 +152,8 @@ moe_status_t gemm_fp8(const uint8_t* a, const float* sa, const uint8_t* w, const
     if (st != MOE_OK) return st;
     if (di.sms < 2) return fail(MOE_ERR_UNSUPPORTED, "the fp8 GEMM needs CTA pairs");
     if (M == 0) return MOE_OK;
-    if ((long)M <= 112L * G && (long)M > 48L * G) return launch_fp8<GATEUP, 128>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
-    if ((long)M <= 48L * G) return launch_fp8<GATEUP, 64>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
+    if ((long)M <= 32L * G) return launch_fp8<GATEUP, 64>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
+    if ((long)M <= 112L * G) return launch_fp8<GATEUP, 128>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
     return launch_fp8<GATEUP, 256>(a, sa, w, sw, offsets, G, M, d, f, out, di.sms, stream);
 }
 
