@@ -142,7 +142,8 @@ struct RowRing {
         if constexpr (RING) {
             if (++stage == stages) stage = 0;
             if (stage == 0) phase ^= 1u;
-            mbar_wait_within(&full[stage], phase, abort_flag, limit);
+            if (!mbar_wait_within(&full[stage], phase, abort_flag, limit) && threadIdx.x == 0 && row < next)
+                mbar_wait_drain(&full[stage], phase);  // no copy is in flight when the CTA leaves
         }
         return true;
     }
