@@ -21,9 +21,20 @@
 // a launch. Rows by plain loads, a barrier between rows: 28.9, 238, 42.3.
 #pragma once
 #include "common.cuh"
+#include "fp8_quant.cuh"
 #include "sync.cuh"
 
 namespace moe {
+
+__device__ __forceinline__ void unpair(const uint64_t (&v)[4], float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("mov.b64 {%0, %1}, %2;" : "=f"(f[2 * i]), "=f"(f[2 * i + 1]) : "l"(v[i]));
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    return lo + hi;
+}
 
 // 8 consecutive elements as they lie in memory
 template <typename E>
@@ -46,6 +57,18 @@ struct Vec8<__nv_bfloat16> {
         q = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }
     __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = q; }
+    __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const {
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = pair2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    }
+    __device__ __forceinline__ void put_pairs(const uint64_t (&v)[4]) {
+        float f[8];
+        unpair(v, f);
+        put(f);
+    }
+    // from here on the values are what this register holds: their fp32 forms are made again, not kept
+    __device__ __forceinline__ void keep_packed() { asm volatile("" : "+r"(q.x), "+r"(q.y), "+r"(q.z), "+r"(q.w)); }
 };
 template <>
 struct Vec8<float> {
@@ -66,20 +89,29 @@ struct Vec8<float> {
         reinterpret_cast<float4*>(p)[0] = a;
         reinterpret_cast<float4*>(p)[1] = b;
     }
+    __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const {
+        v[0] = pair2(a.x, a.y), v[1] = pair2(a.z, a.w), v[2] = pair2(b.x, b.y), v[3] = pair2(b.z, b.w);
+    }
+    __device__ __forceinline__ void put_pairs(const uint64_t (&v)[4]) {
+        float f[8];
+        unpair(v, f);
+        put(f);
+    }
+    __device__ __forceinline__ void keep_packed() {}
 };
 
 constexpr int BN_MAX_THREADS = 512;
 constexpr int BN_MAX_WARPS = BN_MAX_THREADS / 32;
 constexpr int BN_MAX_D = BN_MAX_THREADS * 4 * 8;  // 4 vectors per thread
 constexpr int BN_MAX_STAGES = 8;
+constexpr int BN_MAX_CLUSTER = 8;
 constexpr int BN_GRAD_CTAS = 296;  // rows of a backward pass are cut into at most so many ranges (2 per SM)
 
-// One of the arrays that make up a row's input: row t is the `bytes` from base + t / per * bytes (per > 1: a gate row shared by
-// consecutive tokens).
+// One of the arrays that make up a row's input: elements of `size` bytes (0: no such array); row t is row t / per of it (per > 1: a gate
+// row shared by consecutive tokens).
 struct RowArray {
     const void* base;
-    uint32_t bytes;
-    int per;
+    int size, per;
 };
 
 // Ring of rows in shared memory. RING = false: the same interface on the arrays themselves.
@@ -89,14 +121,18 @@ struct RowRing {
     uint64_t* full;
     volatile int* abort_flag;
     uint8_t* data;
+    int cols, col0, n;  // columns of the arrays, the first one taken, how many
     uint32_t row_bytes;
     int stages, stage, step, end, next;  // next: the row to copy next
     uint32_t phase;
     uint64_t limit;
     int row;
 
-    // rows first, first + step, ... < end
-    __device__ __forceinline__ void start(uint8_t* smem, int n_stages, int first, int step_, int end_) {
+    // columns c0 .. c0 + n_cols of d, rows first, first + step, ... < end
+    __device__ __forceinline__ void start(uint8_t* smem, int n_stages, int d, int c0, int n_cols, int first, int step_, int end_) {
+        cols = d;
+        col0 = c0;
+        n = n_cols;
         step = step_;
         end = end_;
         row = first - step_;
@@ -111,7 +147,7 @@ struct RowRing {
             limit = wait_limit_ns();
             row_bytes = 0;
 #pragma unroll
-            for (int i = 0; i < NARR; ++i) row_bytes += arr[i].bytes;
+            for (int i = 0; i < NARR; ++i) row_bytes += (uint32_t)(n * arr[i].size);
             if (threadIdx.x == 0) {
                 for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
                 *abort_flag = 0;
@@ -127,10 +163,11 @@ struct RowRing {
         uint8_t* to = data + (size_t)s * row_bytes;
 #pragma unroll
         for (int i = 0; i < NARR; ++i) {
-            if (arr[i].bytes == 0) continue;
+            if (arr[i].size == 0) continue;
             const int r = arr[i].per > 1 ? next / arr[i].per : next;
-            bulk_load(to, reinterpret_cast<const uint8_t*>(arr[i].base) + (size_t)r * arr[i].bytes, arr[i].bytes, &full[s]);
-            to += arr[i].bytes;
+            const uint32_t bytes = (uint32_t)(n * arr[i].size);
+            bulk_load(to, reinterpret_cast<const uint8_t*>(arr[i].base) + ((size_t)r * cols + col0) * arr[i].size, bytes, &full[s]);
+            to += bytes;
         }
         next += step;
     }
@@ -154,11 +191,11 @@ struct RowRing {
             uint32_t at = 0;
 #pragma unroll
             for (int j = 0; j < NARR; ++j)
-                if (j < i) at += arr[j].bytes;
+                if (j < i) at += (uint32_t)(n * arr[j].size);
             return reinterpret_cast<const E*>(data + (size_t)stage * row_bytes + at);
         } else {
             const int r = arr[i].per > 1 ? row / arr[i].per : row;
-            return reinterpret_cast<const E*>(reinterpret_cast<const uint8_t*>(arr[i].base) + (size_t)r * arr[i].bytes);
+            return reinterpret_cast<const E*>(reinterpret_cast<const uint8_t*>(arr[i].base) + ((size_t)r * cols + col0) * arr[i].size);
         }
     }
     // The CTA has the current row in registers (all its threads are past a barrier since): its stage takes another
@@ -169,24 +206,71 @@ struct RowRing {
     }
 };
 
-// Sums of NS values over the CTA, given to every thread. `red` is one of two alternating buffers, so one barrier per call
-// suffices: a thread that is a call ahead writes the other buffer, and two calls ahead is past the next barrier.
-template <int NS>
-__device__ __forceinline__ void block_sums(float (&v)[NS], float (*red)[BN_MAX_WARPS]) {
+// Sum over the CTA, given to every thread. `red` is one of two alternating buffers, so one barrier per call suffices: a thread that is
+// a call ahead writes the other buffer, and two calls ahead is past the next barrier.
+__device__ __forceinline__ float block_sum(float v, float* red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        if (lane == 0) red[i][warp] = v[i];
-    }
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) red[warp] = v;
     __syncthreads();
+    float s = (lane & 15) < warps ? red[lane & 15] : 0.f;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        float s = lane < warps ? red[i][lane] : 0.f;
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+// Three sums in 12 shuffles instead of 27 (they would take a third of a row's time): in the first two steps half of the lanes
+// pass on one value and keep another, so that lanes 8 j .. 8 j + 7 end up adding value j; behind the barrier a lane takes value
+// lane % 4 of warps lane / 4 and lane / 4 + 8.
+__device__ __forceinline__ void block_sums(float (&v)[3], float* red) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const bool hi = lane & 16, odd = lane & 8;
+    float x = hi ? v[2] : v[0], y = hi ? 0.f : v[1];
+    x += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+    y += __shfl_xor_sync(0xffffffffu, hi ? v[1] : 0.f, 16);
+    float z = odd ? y : x;
+    z += __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        v[i] = s;
+    for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if ((lane & 7) == 0) red[warp * 4 + (lane >> 3)] = z;
+    __syncthreads();
+    z = (lane >> 2) < warps ? red[lane] : 0.f;
+    if ((lane >> 2) + 8 < warps) z += red[lane + 32];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) v[j] = __shfl_sync(0xffffffffu, z, j);
+}
+
+// Rows wider than a CTA's threads hold are cut by columns over the CTAs of a cluster. Each sends its sums to all of them (st.async into
+// shared memory, counted by the receiver's barrier) and adds what it got in the order of the CTAs. Two slots suffice: a CTA sends its sums
+// of row i + 2 only with those of row i + 1 from every other, which a CTA sends only once its threads are done with row i's.
+struct ClusterSums {
+    float4 slot[2][BN_MAX_CLUSTER];
+    uint64_t bar[2];
+    int abort_flag;
+};
+__device__ __forceinline__ void cluster_sums_init(ClusterSums& x) {
+    if (threadIdx.x == 0) {
+        mbar_init(&x.bar[0], 1);
+        mbar_init(&x.bar[1], 1);
+        x.abort_flag = 0;
+        fence_mbar_init();
+    }
+    cluster_sync();
+}
+// n: how many rows came before
+__device__ __forceinline__ void cluster_sums(ClusterSums& x, int n, uint32_t ctas, uint32_t rank, uint64_t limit, float (&v)[3]) {
+    const int turn = n & 1;
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&x.bar[turn], ctas * 16u);
+    if (threadIdx.x < ctas)
+        store_remote(mapa_shared(smem_u32(&x.slot[turn][rank]), threadIdx.x), make_float4(v[0], v[1], v[2], 0.f),
+                     mapa_shared(smem_u32(&x.bar[turn]), threadIdx.x));
+    mbar_wait_within(&x.bar[turn], (uint32_t)(n >> 1) & 1u, &x.abort_flag, limit);
+    v[0] = v[1] = v[2] = 0.f;
+    for (uint32_t r = 0; r < ctas; ++r) {
+        const float4 q = x.slot[turn][r];
+        v[0] += q.x, v[1] += q.y, v[2] += q.z;
     }
 }
 
@@ -202,6 +286,13 @@ __device__ __forceinline__ void load_gains(const float* w, int nvec, float (&g)[
     }
 }
 
+__device__ __forceinline__ void load_gains(const float* w, int nvec, uint64_t (&g)[4]) {
+    Vec8<float> q;
+    q.zero();
+    if (threadIdx.x < nvec) q.load(w + (size_t)threadIdx.x * 8);
+    q.pairs(g);
+}
+
 // ---- forward ----------------------------------------------------------------------------------------
 
 template <typename R, int VPT, bool RING>
@@ -209,13 +300,13 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_kernel(const R* 
                                                              int d, float eps, __nv_bfloat16* __restrict__ xn,
                                                              float* __restrict__ rstd, int stages) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[2][1][BN_MAX_WARPS];
+    __shared__ float red[2][BN_MAX_WARPS];
     grid_dep_wait();
     grid_dep_trigger();
     const int nvec = d >> 3;
     RowRing<RING, 1> rows;
-    rows.arr[0] = {x, (uint32_t)(d * sizeof(R)), 1};
-    rows.start(smem, stages, blockIdx.x, gridDim.x, T);
+    rows.arr[0] = {x, sizeof(R), 1};
+    rows.start(smem, stages, d, 0, d, blockIdx.x, gridDim.x, T);
     float g[VPT][8];
     load_gains<VPT>(w, nvec, g);
     int turn = 0;
@@ -237,7 +328,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_kernel(const R* 
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[0] = fmaf(f[i], f[i], s[0]);
         }
-        block_sums<1>(s, red[turn]);
+        s[0] = block_sum(s[0], red[turn]);
         rows.release();
         const float rs = rsqrtf(s[0] / (float)d + eps);
         if (threadIdx.x == 0) rstd[t] = rs;
@@ -273,15 +364,15 @@ struct NormOutArgs {
 template <typename R, int VPT, bool NEXT, bool RING>
 __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_kernel(const NormOutArgs a, int stages) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[2][1][BN_MAX_WARPS];
+    __shared__ float red[2][BN_MAX_WARPS];
     grid_dep_wait();
     grid_dep_trigger();
     const int nvec = a.d >> 3;
     RowRing<RING, 3> rows;
-    rows.arr[0] = {a.y, (uint32_t)(a.d * 2), 1};
-    rows.arr[1] = {a.r, (uint32_t)(a.d * sizeof(R)), 1};
-    rows.arr[2] = {a.gate, a.gate ? (uint32_t)(a.d * 2) : 0u, a.gate_rows};
-    rows.start(smem, stages, blockIdx.x, gridDim.x, a.T);
+    rows.arr[0] = {a.y, 2, 1};
+    rows.arr[1] = {a.r, sizeof(R), 1};
+    rows.arr[2] = {a.gate, a.gate ? 2 : 0, a.gate_rows};
+    rows.start(smem, stages, a.d, 0, a.d, blockIdx.x, gridDim.x, a.T);
     float g[VPT][8], gn[NEXT ? VPT : 1][8];
     load_gains<VPT>(a.w, nvec, g);
     if constexpr (NEXT) load_gains<VPT>(a.w_next, nvec, gn);
@@ -313,7 +404,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_kernel(const No
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[0] = fmaf(f[i], f[i], s[0]);
         }
-        block_sums<1>(s, red[turn]);
+        s[0] = block_sum(s[0], red[turn]);
         rows.release();
         turn ^= 1;
         const float rs = rsqrtf(s[0] / (float)a.d + a.eps);
@@ -342,7 +433,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_kernel(const No
             }
         }
         if constexpr (NEXT) {
-            block_sums<1>(s, red[turn]);
+            s[0] = block_sum(s[0], red[turn]);
             turn ^= 1;
             const float rn = rsqrtf(s[0] / (float)a.d + a.eps);
             if (threadIdx.x == 0) a.rstd_next[t] = rn;
@@ -384,14 +475,14 @@ struct NormInGradArgs {
 template <typename R, int VPT, bool RING>
 __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_grad_kernel(const NormInGradArgs a, int stages) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[2][1][BN_MAX_WARPS];
+    __shared__ float red[2][BN_MAX_WARPS];
     const int nvec = a.d >> 3;
     const float inv_d = 1.f / (float)a.d;
     RowRing<RING, 3> rows;
-    rows.arr[0] = {a.dxn, (uint32_t)(a.d * 2), 1};
-    rows.arr[1] = {a.x, (uint32_t)(a.d * sizeof(R)), 1};
-    rows.arr[2] = {a.dres, a.dres ? (uint32_t)(a.d * sizeof(R)) : 0u, 1};
-    rows.start(smem, stages, norm_first_row(a.T, gridDim.x, blockIdx.x), 1, norm_first_row(a.T, gridDim.x, blockIdx.x + 1));
+    rows.arr[0] = {a.dxn, 2, 1};
+    rows.arr[1] = {a.x, sizeof(R), 1};
+    rows.arr[2] = {a.dres, a.dres ? (int)sizeof(R) : 0, 1};
+    rows.start(smem, stages, a.d, 0, a.d, norm_first_row(a.T, gridDim.x, blockIdx.x), 1, norm_first_row(a.T, gridDim.x, blockIdx.x + 1));
     float g[VPT][8], acc[VPT][8];
     load_gains<VPT>(a.w, nvec, g);
 #pragma unroll
@@ -432,7 +523,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_grad_kernel(cons
                 s[0] = fmaf(m[i] * g[u][i], hat, s[0]);
             }
         }
-        block_sums<1>(s, red[turn]);
+        s[0] = block_sum(s[0], red[turn]);
         rows.release();
         const float mean = s[0] * inv_d;
 #pragma unroll
@@ -484,144 +575,156 @@ struct NormOutGradArgs {
 //   dy = rstd (dR g w - yhat S2 / d),                  S2 = sum dR g w yhat,  yhat = y rstd
 // S2 needs dR, which needs S1; but it is linear in it: S2 = SA - (rstd'^3 S1 / d) SB with SA = sum (dout + rstd' dxn w') g w
 // yhat and SB = sum out g w yhat, so one reduction over the row gives all three. dR is never rounded.
-template <typename R, int VPT, bool NEXT, bool GATE, bool RING>
+//
+// A thread keeps one vector of 8 columns: gains, sums and a row's values are up to 80 registers for it. Rows of more columns than
+// a CTA's threads hold are cut over the CTAs of a cluster. (With two vectors per thread they spilled: 4096 rows of 8192 in
+// bf16 202 us, 2048 of 16384 in fp32 921 us.)
+template <typename R, bool NEXT, bool GATE, bool RING, bool CLUSTER>
 __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(const NormOutGradArgs a, int stages) {
-    constexpr int NS = NEXT ? 3 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float red[2][NS][BN_MAX_WARPS];
-    const int nvec = a.d >> 3;
+    __shared__ float red[2][4 * BN_MAX_WARPS];
+    __shared__ __align__(16) ClusterSums across;
+    const uint32_t ctas = CLUSTER ? cluster_nctarank() : 1, rank = CLUSTER ? cluster_ctarank() : 0;
+    const int range = CLUSTER ? blockIdx.x / ctas : blockIdx.x, ranges = CLUSTER ? gridDim.x / ctas : gridDim.x;
+    const int per_cta = ((a.d >> 3) + (int)ctas - 1) / (int)ctas;  // vectors
+    const int c0 = (int)rank * per_cta * 8;                        // this CTA's columns: c0 .. c0 + 8 nvec
+    const int nvec = min(per_cta, (a.d - c0) >> 3);
     const float inv_d = 1.f / (float)a.d;
-    float g[VPT][8], gn[NEXT ? VPT : 1][8];
-    float acc[VPT][8], acc_next[NEXT ? VPT : 1][8], acc_gate[GATE ? VPT : 1][8];
-    const int t0 = norm_first_row(a.T, gridDim.x, blockIdx.x), t1 = norm_first_row(a.T, gridDim.x, blockIdx.x + 1);
+    const int t0 = norm_first_row(a.T, ranges, range), t1 = norm_first_row(a.T, ranges, range + 1);
     RowRing<RING, 5> rows;
-    rows.arr[0] = {a.dout, (uint32_t)(a.d * sizeof(R)), 1};
-    rows.arr[1] = {a.y, (uint32_t)(a.d * 2), 1};
-    rows.arr[2] = {a.out, NEXT ? (uint32_t)(a.d * sizeof(R)) : 0u, 1};
-    rows.arr[3] = {a.dxn, NEXT ? (uint32_t)(a.d * 2) : 0u, 1};
-    rows.arr[4] = {a.gate, GATE ? (uint32_t)(a.d * 2) : 0u, a.gate_rows};
-    rows.start(smem, stages, t0, 1, t1);
-    load_gains<VPT>(a.w, nvec, g);
-    if constexpr (NEXT) load_gains<VPT>(a.w_next, nvec, gn);
+    rows.arr[0] = {a.dout, sizeof(R), 1};
+    rows.arr[1] = {a.y, 2, 1};
+    rows.arr[2] = {a.out, NEXT ? (int)sizeof(R) : 0, 1};
+    rows.arr[3] = {a.dxn, NEXT ? 2 : 0, 1};
+    rows.arr[4] = {a.gate, GATE ? 2 : 0, a.gate_rows};
+    rows.start(smem, stages, a.d, c0, nvec * 8, t0, 1, t1);
+    uint64_t limit = 0;
+    if constexpr (CLUSTER) {
+        limit = wait_limit_ns();
+        cluster_sums_init(across);
+    }
+    // two columns to an operation throughout (fp32 pairs): a row is 1.9 us of a CTA's instructions and latencies otherwise
+    uint64_t g[4], gn[4], acc[4], acc_next[4], acc_gate[4];
+    load_gains(a.w + c0, nvec, g);
+    if constexpr (NEXT) load_gains(a.w_next + c0, nvec, gn);
 #pragma unroll
-    for (int u = 0; u < VPT; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            acc[u][i] = 0.f;
-            if constexpr (NEXT) acc_next[u][i] = 0.f;
-            if constexpr (GATE) acc_gate[u][i] = 0.f;
-        }
-    R* dr = reinterpret_cast<R*>(a.dr);
-    int turn = 0;
-    for (; rows.advance(); turn ^= 1) {
+    for (int i = 0; i < 4; ++i) acc[i] = acc_next[i] = acc_gate[i] = 0;
+    const int v = threadIdx.x;
+    const bool mine = v < nvec;
+    const uint64_t alpha2 = pair2(a.alpha, a.alpha);
+    R* dr = reinterpret_cast<R*>(a.dr) + c0 + v * 8;
+    __nv_bfloat16* dy = a.dy + c0 + v * 8;
+    for (int n = 0; rows.advance(); ++n) {
         const int t = rows.row;
-        Vec8<__nv_bfloat16> dn[NEXT ? VPT : 1], y[VPT], gt[GATE ? VPT : 1];
-        Vec8<R> up[VPT], o[NEXT ? VPT : 1];
-        float s[NS] = {};
+        Vec8<__nv_bfloat16> dn, y, gt;
+        Vec8<R> up, o;
+        float s[3] = {};
         const float rs = a.rstd[t];
         const float rn = NEXT ? a.rstd_next[t] : 0.f;
         const int group = GATE ? t / a.gate_rows : 0;
-#pragma unroll
-        for (int u = 0; u < VPT; ++u) {
-            const int v = threadIdx.x + u * blockDim.x;
-            up[u].zero();
-            y[u].zero();
-            if constexpr (NEXT) o[u].zero(), dn[u].zero();
-            if constexpr (GATE) gt[u].zero();
-            if (v < nvec) {
-                up[u].load(rows.template get<R>(0) + v * 8);
-                y[u].load(rows.template get<__nv_bfloat16>(1) + v * 8);
-                if constexpr (NEXT) {
-                    o[u].load(rows.template get<R>(2) + v * 8);
-                    dn[u].load(rows.template get<__nv_bfloat16>(3) + v * 8);
-                }
-                if constexpr (GATE) gt[u].load(rows.template get<__nv_bfloat16>(4) + v * 8);
+        up.zero();
+        y.zero();
+        if constexpr (NEXT) o.zero(), dn.zero();
+        if constexpr (GATE) gt.zero();
+        if (mine) {
+            up.load(rows.template get<R>(0) + v * 8);
+            y.load(rows.template get<__nv_bfloat16>(1) + v * 8);
+            if constexpr (NEXT) {
+                o.load(rows.template get<R>(2) + v * 8);
+                dn.load(rows.template get<__nv_bfloat16>(3) + v * 8);
             }
+            if constexpr (GATE) gt.load(rows.template get<__nv_bfloat16>(4) + v * 8);
         }
+        const uint64_t rs2 = pair2(rs, rs), rn2 = pair2(rn, rn);
+        {
+            uint64_t fu[4], fy[4], fo[4], fd[4], fg[4], s2[3] = {0, 0, 0};
+            up.pairs(fu);
+            y.pairs(fy);
+            if constexpr (NEXT) o.pairs(fo), dn.pairs(fd);
+            if constexpr (GATE) gt.pairs(fg);
 #pragma unroll
-        for (int u = 0; u < VPT; ++u) {
-            float fu[8], fy[8], fo[8], fd[8], fg[8];
-            up[u].get(fu);
-            y[u].get(fy);
-            if constexpr (NEXT) o[u].get(fo), dn[u].get(fd);
-            if constexpr (GATE) gt[u].get(fg);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float k = fy[i] * rs * g[u][i] * (GATE ? fg[i] : 1.f);
+            for (int i = 0; i < 4; ++i) {
+                uint64_t k = mul2(mul2(fy[i], rs2), g[i]);
+                if constexpr (GATE) k = mul2(k, fg[i]);
                 if constexpr (NEXT) {
-                    const float n = fd[i] * gn[u][i];
-                    s[0] = fmaf(fmaf(rn, n, fu[i]), k, s[0]);
-                    s[1] = fmaf(n, fo[i], s[1]);
-                    s[2] = fmaf(fo[i], k, s[2]);
-                    acc_next[u][i] = fmaf(fd[i], fo[i] * rn, acc_next[u][i]);
+                    const uint64_t m = mul2(fd[i], gn[i]);
+                    s2[0] = fma2(fma2(rn2, m, fu[i]), k, s2[0]);
+                    s2[1] = fma2(m, fo[i], s2[1]);
+                    s2[2] = fma2(fo[i], k, s2[2]);
+                    acc_next[i] = fma2(fd[i], mul2(fo[i], rn2), acc_next[i]);
                 } else {
-                    s[0] = fmaf(fu[i], k, s[0]);
+                    s2[0] = fma2(fu[i], k, s2[0]);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 3; ++j) s[j] = sum2(s2[j]);
         }
-        block_sums<NS>(s, red[turn]);
+        if constexpr (NEXT) {
+            block_sums(s, red[n & 1]);
+        } else {
+            s[0] = block_sum(s[0], red[n & 1]);
+        }
         rows.release();
+        if constexpr (CLUSTER) cluster_sums(across, n, ctas, rank, limit, s);
         float c = 0.f;  // dR = dout + rstd' dxn w' - c out
         if constexpr (NEXT) c = rn * rn * rn * s[1] * inv_d;
-        const float mean = (NEXT ? s[0] - c * s[NS - 1] : s[0]) * inv_d;
+        const float mean = (NEXT ? s[0] - c * s[2] : s[0]) * inv_d;
         const bool last_of_group = GATE && (t + 1 == t1 || (t + 1) % a.gate_rows == 0);
+        if (!mine) continue;
+        up.keep_packed();
+        y.keep_packed();
+        if constexpr (NEXT) o.keep_packed(), dn.keep_packed();
+        if constexpr (GATE) gt.keep_packed();
+        uint64_t fu[4], fy[4], fo[4], fd[4], fg[4];
+        up.pairs(fu);
+        y.pairs(fy);
+        if constexpr (NEXT) o.pairs(fo), dn.pairs(fd);
+        if constexpr (GATE) gt.pairs(fg);
+        const uint64_t minus_c = pair2(-c, -c), minus_mean = pair2(-mean, -mean);
 #pragma unroll
-        for (int u = 0; u < VPT; ++u) {
-            const int v = threadIdx.x + u * blockDim.x;
-            if (v >= nvec) continue;
-            const size_t at = (size_t)t * a.d + (size_t)v * 8;
-            float fu[8], fy[8], fo[8], fd[8], fg[8];
-            up[u].get(fu);
-            y[u].get(fy);
-            if constexpr (NEXT) o[u].get(fo), dn[u].get(fd);
-            if constexpr (GATE) gt[u].get(fg);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float dR = fu[i];
-                if constexpr (NEXT) dR = fmaf(-c, fo[i], fmaf(rn * gn[u][i], fd[i], dR));
-                const float hat = fy[i] * rs;
-                const float e = dR * hat;
-                if constexpr (GATE) {
-                    acc_gate[u][i] = fmaf(e, g[u][i], acc_gate[u][i]);
-                    acc[u][i] = fmaf(e, fg[i], acc[u][i]);
-                    fy[i] = rs * fmaf(-hat, mean, dR * fg[i] * g[u][i]);
-                } else {
-                    acc[u][i] += e;
-                    fy[i] = rs * fmaf(-hat, mean, dR * g[u][i]);
-                }
-                fu[i] = a.alpha * dR;
-            }
-            up[u].put(fu);
-            up[u].store(dr + at);
-            y[u].put(fy);
-            y[u].store(a.dy + at);
+        for (int i = 0; i < 4; ++i) {
+            uint64_t dR = fu[i];
+            if constexpr (NEXT) dR = fma2(minus_c, fo[i], fma2(mul2(rn2, gn[i]), fd[i], dR));
+            const uint64_t hat = mul2(fy[i], rs2), e = mul2(dR, hat);
+            uint64_t dn_i = mul2(dR, g[i]);
             if constexpr (GATE) {
-                if (last_of_group) {
-                    const long g0 = (long)group * a.gate_rows;
-                    const bool whole = g0 >= t0 && (t + 1 == a.T || t + 1 == g0 + a.gate_rows);
-                    float* to = whole ? a.dgate + (size_t)group * a.d
-                                      : a.part_gate + ((size_t)blockIdx.x * 2 + (group == t0 / a.gate_rows ? 0 : 1)) * a.d;
-                    Vec8<float> q;
-                    q.put(acc_gate[u]);
-                    q.store(to + (size_t)v * 8);
+                acc_gate[i] = fma2(e, g[i], acc_gate[i]);
+                acc[i] = fma2(e, fg[i], acc[i]);
+                dn_i = mul2(dn_i, fg[i]);
+            } else {
+                acc[i] = add2(acc[i], e);
+            }
+            fy[i] = mul2(rs2, fma2(hat, minus_mean, dn_i));
+            fu[i] = mul2(alpha2, dR);
+        }
+        up.put_pairs(fu);
+        up.store(dr + (size_t)t * a.d);
+        y.put_pairs(fy);
+        y.store(dy + (size_t)t * a.d);
+        if constexpr (GATE) {
+            if (last_of_group) {
+                const long g0 = (long)group * a.gate_rows;
+                const bool whole = g0 >= t0 && (t + 1 == a.T || t + 1 == g0 + a.gate_rows);
+                float* to = whole ? a.dgate + (size_t)group * a.d
+                                  : a.part_gate + ((size_t)range * 2 + (group == t0 / a.gate_rows ? 0 : 1)) * a.d;
+                Vec8<float> q;
+                q.put_pairs(acc_gate);
+                q.store(to + c0 + v * 8);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc_gate[u][i] = 0.f;
-                }
+                for (int i = 0; i < 4; ++i) acc_gate[i] = 0;
             }
         }
     }
-#pragma unroll
-    for (int u = 0; u < VPT; ++u) {
-        const int v = threadIdx.x + u * blockDim.x;
-        if (v >= nvec) continue;
+    if (mine) {
         Vec8<float> q;
-        q.put(acc[u]);
-        q.store(a.part_w + (size_t)blockIdx.x * a.d + (size_t)v * 8);
+        q.put_pairs(acc);
+        q.store(a.part_w + (size_t)range * a.d + c0 + v * 8);
         if constexpr (NEXT) {
-            q.put(acc_next[u]);
-            q.store(a.part_next + (size_t)blockIdx.x * a.d + (size_t)v * 8);
+            q.put_pairs(acc_next);
+            q.store(a.part_next + (size_t)range * a.d + c0 + v * 8);
         }
     }
+    if constexpr (CLUSTER) cluster_sync();  // no CTA leaves while another's sums may still arrive in it
 }
 
 // Adds up what the CTAs left: blockIdx.y = 0: dw, 1: dw_next (with part_next), then the gate rows that lie in several CTAs, each by

@@ -286,19 +286,69 @@ cudaError_t launch_norm_in_grad(const NormInGradArgs& a, int sms, cudaStream_t s
     return e;
 }
 
+// n: clusters of `ctas` CTAs, one CTA per SM, that are resident at once (asked once per device and size).
+template <typename... KArgs>
+cudaError_t resident_clusters(void (*kernel)(KArgs...), int ctas, int sms, int& n) {
+    n = sms;
+    if (ctas == 1) return cudaSuccess;
+    static int known[kMaxDevices][BN_MAX_CLUSTER + 1] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (known[dev][ctas] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(ctas);
+        cfg.blockDim = dim3(BN_MAX_THREADS);
+        cfg.dynamicSmemBytes = kNormRingBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = ctas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        known[dev][ctas] = std::max(n, 1);
+    }
+    n = known[dev][ctas];
+    return cudaSuccess;
+}
+
+// Columns are cut over a cluster so that a thread has one vector of 8.
+template <typename R, bool NEXT, bool GATE, bool CLUSTER>
+cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int ctas, int sms, cudaStream_t stream, int& B) {
+    const auto ring = block_norm_out_grad_kernel<R, NEXT, GATE, true, CLUSTER>;
+    const auto plain = block_norm_out_grad_kernel<R, NEXT, GATE, false, CLUSTER>;
+    const int per_cta = (a.d / 8 + ctas - 1) / ctas;
+    const size_t row_bytes = (size_t)per_cta * 8 * ((NEXT ? 2 : 1) * (2 + sizeof(R)) + (GATE ? 2 : 0));
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3((per_cta + 31) / 32 * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 1 : 0;
+    int stages = 0;
+    B = a.T;
+    if ((long)a.T * ctas > 2L * sms) {
+        stages = (int)std::min<size_t>(BN_MAX_STAGES, (kNormRingBytes - 1024) / row_bytes);
+        cfg.dynamicSmemBytes = 128 + (size_t)stages * row_bytes;
+        cudaError_t e = norm_smem(ring, kNormRingBytes);
+        if (e == cudaSuccess) e = resident_clusters(ring, ctas, sms, B);
+        if (e != cudaSuccess) return e;
+        B = std::min(B, a.T);
+    }
+    B = std::min(B, BN_GRAD_CTAS);
+    cfg.gridDim = dim3(B * ctas);
+    return cudaLaunchKernelEx(&cfg, stages ? ring : plain, a, stages);
+}
+
 template <typename R, bool NEXT, bool GATE>
 cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int sms, cudaStream_t stream, int& B) {
-    const NormShape s = norm_grad_shape(a.T, a.d, sms, (size_t)a.d * ((NEXT ? 2 : 1) * (2 + sizeof(R)) + (GATE ? 2 : 0)), 1);
-    B = s.grid;
-    cudaError_t e = cudaSuccess;
-#define CALL(V, RING)                                                                                                       \
-    e = norm_smem(block_norm_out_grad_kernel<R, V, NEXT, GATE, RING>, s.smem);                                              \
-    if (e == cudaSuccess)                                                                                                   \
-    e = launch_plain(block_norm_out_grad_kernel<R, V, NEXT, GATE, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream, a,  \
-                     s.stages)
-    MOE_NORM_CASES(s, CALL)
-#undef CALL
-    return e;
+    const int ctas = (a.d / 8 + BN_MAX_THREADS - 1) / BN_MAX_THREADS;
+    return ctas > 1 ? launch_norm_out_grad<R, NEXT, GATE, true>(a, ctas, sms, stream, B)
+                    : launch_norm_out_grad<R, NEXT, GATE, false>(a, ctas, sms, stream, B);
 }
 
 template <typename R>

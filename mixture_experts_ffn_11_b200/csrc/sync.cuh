@@ -56,6 +56,13 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Store 16 bytes into a CTA of the cluster (addresses of mapa_shared): counted on its barrier as transaction bytes.
+__device__ __forceinline__ void store_remote(uint32_t cluster_addr, const float4& v, uint32_t cluster_bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_addr),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(cluster_bar)
+                 : "memory");
+}
+
 // As mbar_wait_bounded, for waits once per K block on several roles' critical paths: the limit is the caller's (read once, by
 // wait_limit_ns() at the kernel's start; reading it in the wait costs an L2 access each time the barrier is not ready), the clock
 // is looked at only after a first poll, and each poll sleeps in hardware for up to 20 us instead of spinning.
