@@ -114,8 +114,11 @@ struct RowArray {
     int size, per;
 };
 
-// Ring of rows in shared memory. RING = false: the same interface on the arrays themselves.
-template <bool RING, int NARR>
+// Ring of rows in shared memory. RING = false: the same interface on the arrays themselves. SPREAD: every warp up to the number
+// of arrays issues one array's copy, else thread 0 all of them (which of the two is
+// faster was measured kernel by kernel: 4096 rows of 8192 in fp32 in two CTAs 192 us by one thread, 147 us spread; 8192 rows of 4096 in
+// bf16 in one CTA 94 and 103 us).
+template <bool RING, int NARR, bool SPREAD = false>
 struct RowRing {
     RowArray arr[NARR];
     uint64_t* full;
@@ -152,22 +155,26 @@ struct RowRing {
                 for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
                 *abort_flag = 0;
                 fence_mbar_init();
-                for (int s = 0; s < stages; ++s) copy(s);
             }
             __syncthreads();
+            for (int s = 0; s < stages; ++s) copy(s);
         }
     }
-    __device__ __forceinline__ void copy(int s) {  // the next row into stage s (one thread)
+    __device__ __forceinline__ void copy(int s) {  // the next row into stage s
         if (next >= end || *abort_flag) return;
-        mbar_arrive_expect_tx(&full[s], row_bytes);
-        uint8_t* to = data + (size_t)s * row_bytes;
+        const int warp = threadIdx.x >> 5;
+        if (SPREAD ? (threadIdx.x & 31) == 0 : threadIdx.x == 0) {
+            if (warp == 0) mbar_arrive_expect_tx(&full[s], row_bytes);
+            uint8_t* to = data + (size_t)s * row_bytes;
 #pragma unroll
-        for (int i = 0; i < NARR; ++i) {
-            if (arr[i].size == 0) continue;
-            const int r = arr[i].per > 1 ? next / arr[i].per : next;
-            const uint32_t bytes = (uint32_t)(n * arr[i].size);
-            bulk_load(to, reinterpret_cast<const uint8_t*>(arr[i].base) + ((size_t)r * cols + col0) * arr[i].size, bytes, &full[s]);
-            to += bytes;
+            for (int i = 0; i < NARR; ++i) {
+                const uint32_t bytes = (uint32_t)(n * arr[i].size);
+                if (arr[i].size != 0 && (!SPREAD || warp == i)) {
+                    const int r = arr[i].per > 1 ? next / arr[i].per : next;
+                    bulk_load(to, reinterpret_cast<const uint8_t*>(arr[i].base) + ((size_t)r * cols + col0) * arr[i].size, bytes, &full[s]);
+                }
+                to += bytes;
+            }
         }
         next += step;
     }
@@ -184,24 +191,31 @@ struct RowRing {
         }
         return true;
     }
-    // Elements of array i of the current row
+    // Where the current row lies, for get() and release() now or some rows later (until it is released)
+    __device__ __forceinline__ int here() const { return RING ? stage : row; }
+    // Elements of array i of the current row, or of the row that was at `at`
     template <typename E>
     __device__ __forceinline__ const E* get(int i) const {
+        return get<E>(i, here());
+    }
+    template <typename E>
+    __device__ __forceinline__ const E* get(int i, int at_row) const {
         if constexpr (RING) {
             uint32_t at = 0;
 #pragma unroll
             for (int j = 0; j < NARR; ++j)
                 if (j < i) at += (uint32_t)(n * arr[j].size);
-            return reinterpret_cast<const E*>(data + (size_t)stage * row_bytes + at);
+            return reinterpret_cast<const E*>(data + (size_t)at_row * row_bytes + at);
         } else {
-            const int r = arr[i].per > 1 ? row / arr[i].per : row;
+            const int r = arr[i].per > 1 ? at_row / arr[i].per : at_row;
             return reinterpret_cast<const E*>(reinterpret_cast<const uint8_t*>(arr[i].base) + ((size_t)r * cols + col0) * arr[i].size);
         }
     }
-    // The CTA has the current row in registers (all its threads are past a barrier since): its stage takes another
-    __device__ __forceinline__ void release() {
+    // The CTA is done with a row (all its threads are past a barrier since they read it): its stage takes another
+    __device__ __forceinline__ void release() { release(here()); }
+    __device__ __forceinline__ void release(int at_row) {
         if constexpr (RING) {
-            if (threadIdx.x == 0) copy(stage);
+            copy(at_row);
         }
     }
 };
@@ -242,31 +256,35 @@ __device__ __forceinline__ void block_sums(float (&v)[3], float* red) {
     for (int j = 0; j < 3; ++j) v[j] = __shfl_sync(0xffffffffu, z, j);
 }
 
-// Rows wider than a CTA's threads hold are cut by columns over the CTAs of a cluster. Each sends its sums to all of them (st.async into
-// shared memory, counted by the receiver's barrier) and adds what it got in the order of the CTAs. Two slots suffice: a CTA sends its sums
-// of row i + 2 only with those of row i + 1 from every other, which a CTA sends only once its threads are done with row i's.
+// Rows wider than a CTA's threads hold are cut by columns over the CTAs of a cluster. Each sends its sums of a row to all of them (st.async
+// into shared memory, counted by the receiver's barrier) and adds what it got in the order of the CTAs, one row later: about 1 us on
+// the way, in which the CTA takes up the next row. Four slots: a CTA sends row m only with every other's sums of row m - 2,
+// which that one sends once all its threads have taken those of row m - 4.
 struct ClusterSums {
-    float4 slot[2][BN_MAX_CLUSTER];
-    uint64_t bar[2];
+    float4 slot[4][BN_MAX_CLUSTER];
+    uint64_t bar[4];
     int abort_flag;
 };
 __device__ __forceinline__ void cluster_sums_init(ClusterSums& x) {
     if (threadIdx.x == 0) {
-        mbar_init(&x.bar[0], 1);
-        mbar_init(&x.bar[1], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&x.bar[i], 1);
         x.abort_flag = 0;
         fence_mbar_init();
     }
     cluster_sync();
 }
 // n: how many rows came before
-__device__ __forceinline__ void cluster_sums(ClusterSums& x, int n, uint32_t ctas, uint32_t rank, uint64_t limit, float (&v)[3]) {
-    const int turn = n & 1;
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(&x.bar[turn], ctas * 16u);
-    if (threadIdx.x < ctas)
-        store_remote(mapa_shared(smem_u32(&x.slot[turn][rank]), threadIdx.x), make_float4(v[0], v[1], v[2], 0.f),
-                     mapa_shared(smem_u32(&x.bar[turn]), threadIdx.x));
-    mbar_wait_within(&x.bar[turn], (uint32_t)(n >> 1) & 1u, &x.abort_flag, limit);
+__device__ __forceinline__ void cluster_sums_send(ClusterSums& x, int n, uint32_t ctas, uint32_t rank, const float (&v)[3]) {
+    const int turn = n & 3;
+    const int i = (int)threadIdx.x - (int)blockDim.x + 32;  // the last warp
+    if (i == 0) mbar_arrive_expect_tx(&x.bar[turn], ctas * 16u);
+    if (i >= 0 && i < (int)ctas)
+        store_remote(mapa_shared(smem_u32(&x.slot[turn][rank]), i), make_float4(v[0], v[1], v[2], 0.f),
+                     mapa_shared(smem_u32(&x.bar[turn]), i));
+}
+__device__ __forceinline__ void cluster_sums_take(ClusterSums& x, int n, uint32_t ctas, uint64_t limit, float (&v)[3]) {
+    const int turn = n & 3;
+    mbar_wait_within(&x.bar[turn], (uint32_t)(n >> 2) & 1u, &x.abort_flag, limit);
     v[0] = v[1] = v[2] = 0.f;
     for (uint32_t r = 0; r < ctas; ++r) {
         const float4 q = x.slot[turn][r];
@@ -591,7 +609,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
     const int nvec = min(per_cta, (a.d - c0) >> 3);
     const float inv_d = 1.f / (float)a.d;
     const int t0 = norm_first_row(a.T, ranges, range), t1 = norm_first_row(a.T, ranges, range + 1);
-    RowRing<RING, 5> rows;
+    RowRing<RING, 5, CLUSTER> rows;  // (a cluster's CTAs have more than 5 warps)
     rows.arr[0] = {a.dout, sizeof(R), 1};
     rows.arr[1] = {a.y, 2, 1};
     rows.arr[2] = {a.out, NEXT ? (int)sizeof(R) : 0, 1};
@@ -614,105 +632,139 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
     const uint64_t alpha2 = pair2(a.alpha, a.alpha);
     R* dr = reinterpret_cast<R*>(a.dr) + c0 + v * 8;
     __nv_bfloat16* dy = a.dy + c0 + v * 8;
-    for (int n = 0; rows.advance(); ++n) {
-        const int t = rows.row;
+    struct Row {
         Vec8<__nv_bfloat16> dn, y, gt;
         Vec8<R> up, o;
-        float s[3] = {};
-        const float rs = a.rstd[t];
-        const float rn = NEXT ? a.rstd_next[t] : 0.f;
-        const int group = GATE ? t / a.gate_rows : 0;
-        up.zero();
-        y.zero();
-        if constexpr (NEXT) o.zero(), dn.zero();
-        if constexpr (GATE) gt.zero();
-        if (mine) {
-            up.load(rows.template get<R>(0) + v * 8);
-            y.load(rows.template get<__nv_bfloat16>(1) + v * 8);
-            if constexpr (NEXT) {
-                o.load(rows.template get<R>(2) + v * 8);
-                dn.load(rows.template get<__nv_bfloat16>(3) + v * 8);
-            }
-            if constexpr (GATE) gt.load(rows.template get<__nv_bfloat16>(4) + v * 8);
+    };
+    const auto load = [&](Row& q, int at) {
+        q.up.zero();
+        q.y.zero();
+        if constexpr (NEXT) q.o.zero(), q.dn.zero();
+        if constexpr (GATE) q.gt.zero();
+        if (!mine) return;
+        q.up.load(rows.template get<R>(0, at) + v * 8);
+        q.y.load(rows.template get<__nv_bfloat16>(1, at) + v * 8);
+        if constexpr (NEXT) {
+            q.o.load(rows.template get<R>(2, at) + v * 8);
+            q.dn.load(rows.template get<__nv_bfloat16>(3, at) + v * 8);
         }
+        if constexpr (GATE) q.gt.load(rows.template get<__nv_bfloat16>(4, at) + v * 8);
+    };
+    // a row's sums over the CTA's columns; n: how many rows came before
+    const auto sums = [&](const Row& q, float rs, float rn, int n, float (&s)[3]) {
         const uint64_t rs2 = pair2(rs, rs), rn2 = pair2(rn, rn);
-        {
-            uint64_t fu[4], fy[4], fo[4], fd[4], fg[4], s2[3] = {0, 0, 0};
-            up.pairs(fu);
-            y.pairs(fy);
-            if constexpr (NEXT) o.pairs(fo), dn.pairs(fd);
-            if constexpr (GATE) gt.pairs(fg);
+        uint64_t fu[4], fy[4], fo[4], fd[4], fg[4], s2[3] = {0, 0, 0};
+        q.up.pairs(fu);
+        q.y.pairs(fy);
+        if constexpr (NEXT) q.o.pairs(fo), q.dn.pairs(fd);
+        if constexpr (GATE) q.gt.pairs(fg);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint64_t k = mul2(mul2(fy[i], rs2), g[i]);
-                if constexpr (GATE) k = mul2(k, fg[i]);
-                if constexpr (NEXT) {
-                    const uint64_t m = mul2(fd[i], gn[i]);
-                    s2[0] = fma2(fma2(rn2, m, fu[i]), k, s2[0]);
-                    s2[1] = fma2(m, fo[i], s2[1]);
-                    s2[2] = fma2(fo[i], k, s2[2]);
-                    acc_next[i] = fma2(fd[i], mul2(fo[i], rn2), acc_next[i]);
-                } else {
-                    s2[0] = fma2(fu[i], k, s2[0]);
-                }
+        for (int i = 0; i < 4; ++i) {
+            uint64_t k = mul2(mul2(fy[i], rs2), g[i]);
+            if constexpr (GATE) k = mul2(k, fg[i]);
+            if constexpr (NEXT) {
+                const uint64_t m = mul2(fd[i], gn[i]);
+                s2[0] = fma2(fma2(rn2, m, fu[i]), k, s2[0]);
+                s2[1] = fma2(m, fo[i], s2[1]);
+                s2[2] = fma2(fo[i], k, s2[2]);
+                acc_next[i] = fma2(fd[i], mul2(fo[i], rn2), acc_next[i]);
+            } else {
+                s2[0] = fma2(fu[i], k, s2[0]);
             }
-#pragma unroll
-            for (int j = 0; j < 3; ++j) s[j] = sum2(s2[j]);
         }
         if constexpr (NEXT) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j) s[j] = sum2(s2[j]);
             block_sums(s, red[n & 1]);
         } else {
-            s[0] = block_sum(s[0], red[n & 1]);
+            s[0] = block_sum(sum2(s2[0]), red[n & 1]);
+            s[1] = s[2] = 0.f;
         }
-        rows.release();
-        if constexpr (CLUSTER) cluster_sums(across, n, ctas, rank, limit, s);
+    };
+    // its gradients, from the sums over all columns
+    const auto finish = [&](Row& q, int t, float rs, float rn, const float (&s)[3]) {
         float c = 0.f;  // dR = dout + rstd' dxn w' - c out
         if constexpr (NEXT) c = rn * rn * rn * s[1] * inv_d;
         const float mean = (NEXT ? s[0] - c * s[2] : s[0]) * inv_d;
-        const bool last_of_group = GATE && (t + 1 == t1 || (t + 1) % a.gate_rows == 0);
-        if (!mine) continue;
-        up.keep_packed();
-        y.keep_packed();
-        if constexpr (NEXT) o.keep_packed(), dn.keep_packed();
-        if constexpr (GATE) gt.keep_packed();
+        if (!mine) return;
+        q.up.keep_packed();
+        q.y.keep_packed();
+        if constexpr (NEXT) q.o.keep_packed(), q.dn.keep_packed();
+        if constexpr (GATE) q.gt.keep_packed();
         uint64_t fu[4], fy[4], fo[4], fd[4], fg[4];
-        up.pairs(fu);
-        y.pairs(fy);
-        if constexpr (NEXT) o.pairs(fo), dn.pairs(fd);
-        if constexpr (GATE) gt.pairs(fg);
-        const uint64_t minus_c = pair2(-c, -c), minus_mean = pair2(-mean, -mean);
+        q.up.pairs(fu);
+        q.y.pairs(fy);
+        if constexpr (NEXT) q.o.pairs(fo), q.dn.pairs(fd);
+        if constexpr (GATE) q.gt.pairs(fg);
+        const uint64_t rs2 = pair2(rs, rs), rn2 = pair2(rn, rn), minus_c = pair2(-c, -c), minus_mean = pair2(-mean, -mean);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint64_t dR = fu[i];
             if constexpr (NEXT) dR = fma2(minus_c, fo[i], fma2(mul2(rn2, gn[i]), fd[i], dR));
             const uint64_t hat = mul2(fy[i], rs2), e = mul2(dR, hat);
-            uint64_t dn_i = mul2(dR, g[i]);
+            uint64_t dn = mul2(dR, g[i]);
             if constexpr (GATE) {
                 acc_gate[i] = fma2(e, g[i], acc_gate[i]);
                 acc[i] = fma2(e, fg[i], acc[i]);
-                dn_i = mul2(dn_i, fg[i]);
+                dn = mul2(dn, fg[i]);
             } else {
                 acc[i] = add2(acc[i], e);
             }
-            fy[i] = mul2(rs2, fma2(hat, minus_mean, dn_i));
+            fy[i] = mul2(rs2, fma2(hat, minus_mean, dn));
             fu[i] = mul2(alpha2, dR);
         }
-        up.put_pairs(fu);
-        up.store(dr + (size_t)t * a.d);
-        y.put_pairs(fy);
-        y.store(dy + (size_t)t * a.d);
+        q.up.put_pairs(fu);
+        q.up.store(dr + (size_t)t * a.d);
+        q.y.put_pairs(fy);
+        q.y.store(dy + (size_t)t * a.d);
         if constexpr (GATE) {
-            if (last_of_group) {
+            if (t + 1 == t1 || (t + 1) % a.gate_rows == 0) {  // the last of a gate row's tokens here
+                const int group = t / a.gate_rows;
                 const long g0 = (long)group * a.gate_rows;
                 const bool whole = g0 >= t0 && (t + 1 == a.T || t + 1 == g0 + a.gate_rows);
                 float* to = whole ? a.dgate + (size_t)group * a.d
                                   : a.part_gate + ((size_t)range * 2 + (group == t0 / a.gate_rows ? 0 : 1)) * a.d;
-                Vec8<float> q;
-                q.put_pairs(acc_gate);
-                q.store(to + c0 + v * 8);
+                Vec8<float> o;
+                o.put_pairs(acc_gate);
+                o.store(to + c0 + v * 8);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc_gate[i] = 0;
             }
+        }
+    };
+    if constexpr (!CLUSTER) {
+        for (int n = 0; rows.advance(); ++n) {
+            const int t = rows.row;
+            const float rs = a.rstd[t], rn = NEXT ? a.rstd_next[t] : 0.f;
+            Row q;
+            float s[3];
+            load(q, rows.here());
+            sums(q, rs, rn, n, s);
+            rows.release();
+            finish(q, t, rs, rn, s);
+        }
+    } else {
+        int before = 0, before2 = 0;  // where the two rows before lie
+        float rs_before = 0.f, rn_before = 0.f;
+        for (int n = 0;; ++n) {
+            const bool more = rows.advance();
+            float rs = 0.f, rn = 0.f, s[3];
+            Row q;
+            if (more) {
+                rs = a.rstd[rows.row], rn = NEXT ? a.rstd_next[rows.row] : 0.f;
+                load(q, rows.here());
+                sums(q, rs, rn, n, s);
+                cluster_sums_send(across, n, ctas, rank, s);
+                if (n > 1) rows.release(before2);
+            }
+            if (n > 0) {
+                load(q, before);
+                cluster_sums_take(across, n - 1, ctas, limit, s);
+                finish(q, t0 + n - 1, rs_before, rn_before, s);
+            }
+            if (!more) break;
+            before2 = before, before = rows.here();
+            rs_before = rs, rn_before = rn;
         }
     }
     if (mine) {
