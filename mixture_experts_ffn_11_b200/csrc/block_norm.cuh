@@ -16,7 +16,7 @@
 //
 // Measured (HBM's floor at a copy's rate in brackets): behind the block with the next norm, 4096 rows of 2880 in bf16, 24.7 us
 // (14.4; its output mostly stays in L2, a row's reductions and stores set the pace); its gradient, 8192 rows of 4096 with an fp32 stream and
-// a gate, 103-118 us (92); the gradient in front, 4096 rows of 2880, 25.7-30 us (14.4), in two kernels, the second adding the
+// a gate, 109 us (92); the gradient in front, 4096 rows of 2880, 25.7-30 us (14.4), in two kernels, the second adding the
 // CTAs' partial sums in a fixed order (four rows of them at a time; one at a time 28.7 us in all); in front, 64 rows of 7168, 1.9 us (0.3),
 // a launch. Rows by plain loads, a barrier between rows: 28.9, 238, 42.3.
 #pragma once
@@ -233,7 +233,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
-// Three sums in 12 shuffles instead of 27 (they would take a third of a row's time): in the first two steps half of the lanes
+// Three sums in 12 shuffles instead of 27: in the first two steps half of the lanes
 // pass on one value and keep another, so that lanes 8 j .. 8 j + 7 end up adding value j; behind the barrier a lane takes value
 // lane % 4 of warps lane / 4 and lane / 4 + 8.
 __device__ __forceinline__ void block_sums(float (&v)[3], float* red) {
@@ -595,8 +595,9 @@ struct NormOutGradArgs {
 // yhat and SB = sum out g w yhat, so one reduction over the row gives all three. dR is never rounded.
 //
 // A thread keeps one vector of 8 columns: gains, sums and a row's values are up to 80 registers for it. Rows of more columns than
-// a CTA's threads hold are cut over the CTAs of a cluster. (With two vectors per thread they spilled: 4096 rows of 8192 in
-// bf16 202 us, 2048 of 16384 in fp32 921 us.)
+// a CTA's threads hold are cut over the CTAs of a cluster. (With two or four vectors per thread they spilled: 4096 rows of 8192 in
+// bf16 202 us instead of 132, 2048 of 16384 in fp32 921 us instead of 155.) Instructions and the steps from row to row bound it there, HBM
+// for one CTA per row in fp32 (8192 rows of 4096 with gate and next norm: 109 us, floor 92; bf16 89 us, floor 62).
 template <typename R, bool NEXT, bool GATE, bool RING, bool CLUSTER>
 __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(const NormOutGradArgs a, int stages) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
         limit = wait_limit_ns();
         cluster_sums_init(across);
     }
-    // two columns to an operation throughout (fp32 pairs): a row is 1.9 us of a CTA's instructions and latencies otherwise
+    // two columns to an operation throughout (fp32 pairs): a row's instructions weigh as much as its bytes
     uint64_t g[4], gn[4], acc[4], acc_next[4], acc_gate[4];
     load_gains(a.w + c0, nvec, g);
     if constexpr (NEXT) load_gains(a.w_next + c0, nvec, gn);

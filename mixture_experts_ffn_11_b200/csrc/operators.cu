@@ -286,11 +286,10 @@ cudaError_t launch_norm_in_grad(const NormInGradArgs& a, int sms, cudaStream_t s
     return e;
 }
 
-// n: clusters of `ctas` CTAs, one CTA per SM, that are resident at once (asked once per device and size).
+// n: clusters of `ctas` CTAs of `threads` threads and `smem` bytes that are resident at once (asked once per device and cluster size,
+// of whichever kernel comes first: shared memory is what limits them all).
 template <typename... KArgs>
-cudaError_t resident_clusters(void (*kernel)(KArgs...), int ctas, int sms, int& n) {
-    n = sms;
-    if (ctas == 1) return cudaSuccess;
+cudaError_t resident_clusters(void (*kernel)(KArgs...), int ctas, int threads, size_t smem, int& n) {
     static int known[kMaxDevices][BN_MAX_CLUSTER + 1] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -299,8 +298,8 @@ cudaError_t resident_clusters(void (*kernel)(KArgs...), int ctas, int sms, int& 
     if (known[dev][ctas] == 0) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(ctas);
-        cfg.blockDim = dim3(BN_MAX_THREADS);
-        cfg.dynamicSmemBytes = kNormRingBytes;
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = ctas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -313,6 +312,11 @@ cudaError_t resident_clusters(void (*kernel)(KArgs...), int ctas, int sms, int& 
     n = known[dev][ctas];
     return cudaSuccess;
 }
+
+constexpr int kNormPairThreads = BN_MAX_THREADS / 2;  // CTAs of so many threads run two to an SM (their registers allow no more)
+constexpr size_t kNormPairBytes = kNormRingBytes / 2 - 1024;
+// a cluster's CTAs have rows in three stages at a time: fp32 stream, next norm and gate are 14 bytes per column
+static_assert(kNormPairBytes / (kNormPairThreads * 8 * 14) >= 3, "stages");
 
 // Columns are cut over a cluster so that a thread has one vector of 8.
 template <typename R, bool NEXT, bool GATE, bool CLUSTER>
@@ -329,17 +333,18 @@ cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int ctas, int sms, cu
     attr[0].val.clusterDim.x = ctas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CLUSTER ? 1 : 0;
-    // Two CTAs per SM where 256 threads hold a row (their registers allow no more): 8192 rows of 2048 in bf16 50 us, one: 71 us.
-    const int per_sm = per_cta <= BN_MAX_THREADS / 2 ? 2 : 1;
+    // Two CTAs per SM where 256 threads hold a row: 8192 rows of 2048 in bf16 50 us, with one 71 us.
+    const int per_sm = per_cta <= kNormPairThreads ? 2 : 1;
     int stages = 0;
     B = a.T;
     if ((long)a.T * ctas > 2L * sms) {
         stages = (int)std::min<size_t>(BN_MAX_STAGES, (kNormRingBytes / per_sm - 1024) / row_bytes);
         cfg.dynamicSmemBytes = 128 + (size_t)stages * row_bytes;
+        int resident = sms * per_sm;
         cudaError_t e = norm_smem(ring, kNormRingBytes);
-        if (e == cudaSuccess) e = resident_clusters(ring, ctas, sms, B);
+        if (CLUSTER && e == cudaSuccess) e = resident_clusters(ring, ctas, kNormPairThreads, kNormPairBytes, resident);
         if (e != cudaSuccess) return e;
-        B = std::min(B * (CLUSTER ? 1 : per_sm), a.T);
+        B = std::min(resident, a.T);
     }
     B = std::min(B, BN_GRAD_CTAS);
     cfg.gridDim = dim3(B * ctas);
@@ -348,7 +353,9 @@ cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int ctas, int sms, cu
 
 template <typename R, bool NEXT, bool GATE>
 cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int sms, cudaStream_t stream, int& B) {
-    const int ctas = (a.d / 8 + BN_MAX_THREADS - 1) / BN_MAX_THREADS;
+    // Up to 4096 columns one CTA (8192 rows of 4096 in bf16 89 us; two of 256 threads each, 120 to 150 us), above that CTAs of up to 256
+    // threads, two to an SM (6000 rows of 5120 in bf16 139 us, two CTAs of 320 threads 151 us).
+    const int ctas = a.d / 8 <= BN_MAX_THREADS ? 1 : (a.d / 8 + kNormPairThreads - 1) / kNormPairThreads;
     return ctas > 1 ? launch_norm_out_grad<R, NEXT, GATE, true>(a, ctas, sms, stream, B)
                     : launch_norm_out_grad<R, NEXT, GATE, false>(a, ctas, sms, stream, B);
 }
