@@ -195,6 +195,23 @@ def test_norm_out_backward(T, d, rows, res, next_norm):
         assert v is None or torch.equal(v, inplace[name]), name
 
 
+@pytest.mark.parametrize("res", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d,rows", [(149, 4104, 0), (700, 5000, 11), (311, 8192, 1), (601, 8200, 601), (160, 12288, 7), (450, 16384, 200)])
+@pytest.mark.parametrize("next_norm", [True, False])
+def test_norm_out_backward_of_wide_rows(T, d, rows, res, next_norm):
+    """Rows over several CTAs, many of them to each: slices of unequal length, every count of CTAs from 3 to 8; in place and run again."""
+    test_norm_out_backward(T, d, rows, res, next_norm)
+    st = inputs(T, d, res, rows, seed=7)
+    fwd = run_out(st, 1.0)
+    first = run_out_backward(st, fwd, 1.0, next_norm)
+    dout = st["dout"].clone()
+    st["dout"].copy_(dout)
+    again = run_out_backward(st, fwd, 1.0, next_norm, dr=st["dout"])  # in place of dout
+    for name in first:
+        if first[name] is not None:
+            assert torch.equal(first[name], again[name]), name
+
+
 def test_gradients_are_the_formulas_own():
     """The 64-bit formulas above against autograd and central differences of the forward in 64 bits."""
     T, d, rows, alpha = 6, 16, 4, 0.7
