@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_grad_kernel(cons
     rows.arr[0] = {a.dxn, 2, 1};
     rows.arr[1] = {a.x, sizeof(R), 1};
     rows.arr[2] = {a.dres, a.dres ? (int)sizeof(R) : 0, 1};
+    grid_dep_trigger();
     rows.start(smem, stages, a.d, 0, a.d, norm_first_row(a.T, gridDim.x, blockIdx.x), 1, norm_first_row(a.T, gridDim.x, blockIdx.x + 1));
     float g[VPT][8], acc[VPT][8];
     load_gains<VPT>(a.w, nvec, g);
@@ -616,6 +617,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
     rows.arr[2] = {a.out, NEXT ? (int)sizeof(R) : 0, 1};
     rows.arr[3] = {a.dxn, NEXT ? 2 : 0, 1};
     rows.arr[4] = {a.gate, GATE ? 2 : 0, a.gate_rows};
+    grid_dep_trigger();
     rows.start(smem, stages, a.d, c0, nvec * 8, t0, 1, t1);
     uint64_t limit = 0;
     if constexpr (CLUSTER) {
@@ -813,6 +815,7 @@ __global__ void __launch_bounds__(BNR_WARPS * 32) block_norm_reduce_kernel(const
         to = a.dgate + group * a.d;
         pitch *= 2;
     }
+    grid_dep_wait();
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     const int col4 = blockIdx.x * 32 + (lane & 7) * 4;
     if (col4 < a.d) {

@@ -379,7 +379,7 @@ cudaError_t launch_norm_reduce(NormReduceArgs& a, cudaStream_t stream) {
             if (row % a.gate_rows != 0) seen = group;
         }
     }
-    return launch_plain(block_norm_reduce_kernel, dim3((a.d + 31) / 32, a.sums + edges), dim3(BNR_WARPS * 32), 0, stream, a);
+    return launch_pdl(block_norm_reduce_kernel, dim3((a.d + 31) / 32, a.sums + edges), dim3(BNR_WARPS * 32), 0, stream, a);
 }
 
 // Workspace of a backward pass: part_w [B][d] | part_next [B][d] | part_gate [B][2][d] (with a gate)
