@@ -14,11 +14,11 @@
 // reductions; a stage is refilled as soon as the CTA has its row in registers. Few rows (at most one per CTA): plain loads, without
 // the copies' extra latency.
 //
-// Measured (HBM's floor at a copy's rate in brackets): behind the block with the next norm, 4096 rows of 2880 in bf16, 24.7 us
-// (14.4; its output mostly stays in L2, a row's reductions and stores set the pace); its gradient, 8192 rows of 4096 with an fp32 stream and
-// a gate, 109 us (92); the gradient in front, 4096 rows of 2880, 25.7-30 us (14.4), in two kernels, the second adding the
-// CTAs' partial sums in a fixed order (four rows of them at a time; one at a time 28.7 us in all); in front, 64 rows of 7168, 1.9 us (0.3),
-// a launch. Rows by plain loads, a barrier between rows: 28.9, 238, 42.3.
+// Measured (HBM's floor at a copy's rate in brackets): behind the block with the next norm, 4096 rows of 2880 in bf16, 25 us (14.4; its
+// output mostly stays in L2, a row's reductions and stores set the pace); its gradient with a gate, 8192 rows of 4096 with an fp32 stream,
+// 109 us (92), in bf16 89 us (62); the gradient in front, 4096 rows of 2880, 25.5 us (14.4), in two kernels, the second, launched ahead,
+// adding the CTAs' partial sums in a fixed order, four rows of them at a time (launched behind the first 30.4 us); in front, 64 rows of
+// 7168, 1.9 us (0.3), a launch. Rows by plain loads, one thread for all of a row's columns: 28.9, 238, -, 42.3.
 #pragma once
 #include "common.cuh"
 #include "fp8_quant.cuh"
@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_in_grad_kernel(cons
     rows.arr[0] = {a.dxn, 2, 1};
     rows.arr[1] = {a.x, sizeof(R), 1};
     rows.arr[2] = {a.dres, a.dres ? (int)sizeof(R) : 0, 1};
+    grid_dep_wait();
     grid_dep_trigger();
     rows.start(smem, stages, a.d, 0, a.d, norm_first_row(a.T, gridDim.x, blockIdx.x), 1, norm_first_row(a.T, gridDim.x, blockIdx.x + 1));
     float g[VPT][8], acc[VPT][8];
@@ -617,6 +618,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
     rows.arr[2] = {a.out, NEXT ? (int)sizeof(R) : 0, 1};
     rows.arr[3] = {a.dxn, NEXT ? 2 : 0, 1};
     rows.arr[4] = {a.gate, GATE ? 2 : 0, a.gate_rows};
+    grid_dep_wait();
     grid_dep_trigger();
     rows.start(smem, stages, a.d, c0, nvec * 8, t0, 1, t1);
     uint64_t limit = 0;
@@ -816,6 +818,7 @@ __global__ void __launch_bounds__(BNR_WARPS * 32) block_norm_reduce_kernel(const
         pitch *= 2;
     }
     grid_dep_wait();
+    grid_dep_trigger();
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     const int col4 = blockIdx.x * 32 + (lane & 7) * 4;
     if (col4 < a.d) {

@@ -280,7 +280,7 @@ cudaError_t launch_norm_in_grad(const NormInGradArgs& a, int sms, cudaStream_t s
 #define CALL(V, RING)                                                                                                    \
     e = norm_smem(block_norm_in_grad_kernel<R, V, RING>, s.smem);                                                        \
     if (e == cudaSuccess)                                                                                                \
-    e = launch_plain(block_norm_in_grad_kernel<R, V, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream, a, s.stages)
+    e = launch_pdl(block_norm_in_grad_kernel<R, V, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream, a, s.stages)
     MOE_NORM_CASES(s, CALL)
 #undef CALL
     return e;
@@ -328,11 +328,13 @@ cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int ctas, int sms, cu
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3((per_cta + 31) / 32 * 32);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // as launch_pdl
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CLUSTER ? 1 : 0;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
     // Two CTAs per SM where 256 threads hold a row: 8192 rows of 2048 in bf16 50 us, with one 71 us.
     const int per_sm = per_cta <= kNormPairThreads ? 2 : 1;
     int stages = 0;
