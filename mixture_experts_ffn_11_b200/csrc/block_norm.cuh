@@ -105,7 +105,7 @@ constexpr int BN_MAX_WARPS = BN_MAX_THREADS / 32;
 constexpr int BN_MAX_D = BN_MAX_THREADS * 4 * 8;  // 4 vectors per thread
 constexpr int BN_MAX_STAGES = 8;
 constexpr int BN_MAX_CLUSTER = 8;
-constexpr int BN_GRAD_CTAS = 296;  // rows of a backward pass are cut into at most so many ranges (2 per SM)
+constexpr int BN_GRAD_CTAS = 592;  // rows of a backward pass are cut into at most so many ranges (4 per SM)
 
 // One of the arrays that make up a row's input: elements of `size` bytes (0: no such array); row t is row t / per of it (per > 1: a gate
 // row shared by consecutive tokens).

@@ -164,13 +164,15 @@ namespace {
 
 // Launch shape for T rows of d columns, row_bytes of input each: vectors per thread, threads, CTAs and stages of the row ring
 // (0: no ring). Up to two rows per SM: a row per CTA by plain loads, one vector per thread where that fits, for the shortest path
-// through a row. More: rings that fill about 200 KB of shared memory per SM between `per_sm` CTAs.
+// through a row. More: rings that fill about 200 KB of shared memory per SM between `per_sm` CTAs, or as many more (up to `most`) as
+// 512 threads make, so that narrow rows too have some 16 warps' work under way (behind the block, 8192 rows of 1024 in bf16: two CTAs of
+// 128 threads per SM 34 us, four 22 us).
 struct NormShape {
     int vpt, threads, grid, stages;
     size_t smem;
 };
 constexpr size_t kNormRingBytes = 204 * 1024;
-NormShape norm_shape(int T, int d, int sms, size_t row_bytes, int vpt1_max, int per_sm) {
+NormShape norm_shape(int T, int d, int sms, size_t row_bytes, int vpt1_max, int per_sm, int most) {
     const int nvec = d / 8;
     NormShape s{};
     const bool ring = T > 2 * sms;
@@ -181,7 +183,7 @@ NormShape norm_shape(int T, int d, int sms, size_t row_bytes, int vpt1_max, int 
         s.grid = T;
         return s;
     }
-    int m = per_sm;
+    int m = std::max(per_sm, std::min(BN_MAX_THREADS / s.threads, most));
     while (m > 1 && (m * s.threads > 1536 || 2 * row_bytes > kNormRingBytes / m)) --m;
     s.grid = m * sms < T ? m * sms : T;
     s.stages = (int)std::min<size_t>(BN_MAX_STAGES, (kNormRingBytes / m - 256) / row_bytes);
@@ -220,7 +222,8 @@ moe_status_t check_norm_gate(const void* gate, int gate_rows, int T) {
     return MOE_OK;
 }
 
-int norm_grad_ctas(int T) { return T < BN_GRAD_CTAS ? T : BN_GRAD_CTAS; }
+// (four CTAs per SM for rows that 128 threads hold, else two)
+int norm_grad_ctas(int T, int d) { return std::min(T, d <= 1024 ? BN_GRAD_CTAS : BN_GRAD_CTAS / 2); }
 
 #define MOE_NORM_CASES(s, CALL)                              \
     if (s.stages) {                                          \
@@ -240,7 +243,7 @@ int norm_grad_ctas(int T) { return T < BN_GRAD_CTAS ? T : BN_GRAD_CTAS; }
 template <typename R>
 cudaError_t launch_norm_in(const void* x, const float* w, int T, int d, float eps, void* xn, float* rstd, int sms,
                            cudaStream_t stream) {
-    const NormShape s = norm_shape(T, d, sms, (size_t)d * sizeof(R), 128, 4);
+    const NormShape s = norm_shape(T, d, sms, (size_t)d * sizeof(R), 128, 4, 8);
     cudaError_t e = cudaSuccess;
 #define CALL(V, RING)                                                                                                      \
     e = norm_smem(block_norm_in_kernel<R, V, RING>, s.smem);                                                               \
@@ -254,7 +257,7 @@ cudaError_t launch_norm_in(const void* x, const float* w, int T, int d, float ep
 
 template <typename R, bool NEXT>
 cudaError_t launch_norm_out(const NormOutArgs& a, int sms, cudaStream_t stream) {
-    const NormShape s = norm_shape(a.T, a.d, sms, (size_t)a.d * (2 + sizeof(R) + (a.gate ? 2 : 0)), 128, 2);
+    const NormShape s = norm_shape(a.T, a.d, sms, (size_t)a.d * (2 + sizeof(R) + (a.gate ? 2 : 0)), 128, 2, 8);
     cudaError_t e = cudaSuccess;
 #define CALL(V, RING)                                                                                                \
     e = norm_smem(block_norm_out_kernel<R, V, NEXT, RING>, s.smem);                                                  \
@@ -265,10 +268,10 @@ cudaError_t launch_norm_out(const NormOutArgs& a, int sms, cudaStream_t stream) 
     return e;
 }
 
-// The backward kernels' grids: at most BN_GRAD_CTAS (the workspace has that many partial rows).
+// The backward kernels' grids: at most norm_grad_ctas(T, d), the partial rows of the workspace.
 NormShape norm_grad_shape(int T, int d, int sms, size_t row_bytes, int per_sm) {
-    NormShape s = norm_shape(T, d, sms, row_bytes, BN_MAX_THREADS, per_sm);
-    if (s.grid > BN_GRAD_CTAS) s.grid = BN_GRAD_CTAS;
+    NormShape s = norm_shape(T, d, sms, row_bytes, BN_MAX_THREADS, per_sm, 4);
+    s.grid = std::min(s.grid, norm_grad_ctas(T, d));
     return s;
 }
 
@@ -335,8 +338,8 @@ cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int ctas, int sms, cu
     attr[1].val.clusterDim.x = ctas, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CLUSTER ? 2 : 1;
-    // Two CTAs per SM where 256 threads hold a row: 8192 rows of 2048 in bf16 50 us, with one 71 us.
-    const int per_sm = per_cta <= kNormPairThreads ? 2 : 1;
+    // Two CTAs per SM where 256 threads hold a row (8192 rows of 2048 in bf16 50 us, with one 71 us), four where 128 do.
+    const int per_sm = std::max(1, std::min(BN_MAX_THREADS / (int)cfg.blockDim.x, 4));
     int stages = 0;
     B = a.T;
     if ((long)a.T * ctas > 2L * sms) {
@@ -348,7 +351,7 @@ cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int ctas, int sms, cu
         if (e != cudaSuccess) return e;
         B = std::min(resident, a.T);
     }
-    B = std::min(B, BN_GRAD_CTAS);
+    B = std::min(B, norm_grad_ctas(a.T, a.d));
     cfg.gridDim = dim3(B * ctas);
     return cudaLaunchKernelEx(&cfg, stages ? ring : plain, a, stages);
 }
@@ -373,19 +376,23 @@ cudaError_t launch_norm_reduce(NormReduceArgs& a, cudaStream_t stream) {
     a.sums = a.part_next ? 2 : 1;
     int edges = 0;
     if (a.part_gate) {
-        long seen = -1;  // gate row of the last edge
+        // row: norm_first_row(T, B, b + 1), the first row behind CTA b, in steps (its divisions took microseconds of the call)
+        const uint32_t step = a.T / a.B, rest = a.T % a.B, rows = a.gate_rows;
+        uint32_t row = 0, over = 0, seen = ~0u;  // seen: gate row of the last edge
         for (int b = 0; b + 1 < a.B; ++b) {
-            const int row = norm_first_row(a.T, a.B, b + 1);  // the first row behind CTA b
-            const long group = row / a.gate_rows;
-            if (row % a.gate_rows != 0 && group != seen) a.edge[edges++] = (int16_t)b;
-            if (row % a.gate_rows != 0) seen = group;
+            row += step;
+            if ((over += rest) >= (uint32_t)a.B) over -= a.B, ++row;
+            const uint32_t group = row / rows;
+            if (row == group * rows) continue;
+            if (group != seen) a.edge[edges++] = (int16_t)b;
+            seen = group;
         }
     }
     return launch_pdl(block_norm_reduce_kernel, dim3((a.d + 31) / 32, a.sums + edges), dim3(BNR_WARPS * 32), 0, stream, a);
 }
 
 // Workspace of a backward pass: part_w [B][d] | part_next [B][d] | part_gate [B][2][d] (with a gate)
-size_t norm_grad_ws(int T, int d, int gate_rows) { return (size_t)norm_grad_ctas(T) * d * 4 * (gate_rows > 0 ? 4 : 2); }
+size_t norm_grad_ws(int T, int d, int gate_rows) { return (size_t)norm_grad_ctas(T, d) * d * 4 * (gate_rows > 0 ? 4 : 2); }
 
 }  // namespace
 
@@ -609,7 +616,7 @@ moe_status_t moe_block_norm_out_backward(const void* dout, const moe_bf16_t* dxn
         if (e == cudaSuccess && dw_next) e = cudaMemsetAsync(dw_next, 0, sizeof(float) * (size_t)d, stream);
         return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
     }
-    int B = norm_grad_ctas(T);
+    int B = norm_grad_ctas(T, d);
     float* part = reinterpret_cast<float*>(ws);
     NormOutGradArgs a{};
     a.dout = dout, a.dxn = reinterpret_cast<const __nv_bfloat16*>(dxn), a.y = reinterpret_cast<const __nv_bfloat16*>(y);
