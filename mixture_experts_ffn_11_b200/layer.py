@@ -565,9 +565,14 @@ class MoEBlock:
     def forward(self, r, xn=None, next_norm=None, gate=None, gate_rows: int = 0, train: bool = False, stream=None):
         """The block's output stream [T, d] (a buffer of the block), or with next_norm (the next block's w_in) the pair (output
         stream, its normed input for the next block). xn: this block's normed input, if the block before made it. gate [ceil(T /
-        gate_rows), d] bf16: a gate for this call, one row per gate_rows tokens. train: keep what backward() reads."""
+        gate_rows), d] bf16: a gate for this call, one row per gate_rows tokens. train: keep what backward() reads; r and xn then may
+        not be this block's own outputs, which the call overwrites."""
         T = r.shape[0]
         b = self._buffers(T, r.dtype)
+        if train and T > 0:
+            store = lambda t: t.untyped_storage().data_ptr()  # noqa: E731
+            if store(r) == store(b["out"]) or (xn is not None and next_norm is not None and store(xn) == store(b["xn_next"])):
+                raise ValueError("backward() reads r and xn, and this forward would overwrite them: they are the block's own outputs")
         if gate is None and self.gate is not None:
             gate, gate_rows = self.gate.view(1, -1)[:min(T, 1)], max(T, 1)
         made = xn is None
@@ -577,7 +582,7 @@ class MoEBlock:
         y = self.ffn.forward(xn, stream, train=train)
         N.block_norm_out(y, r, self.w_out, gate, gate_rows, self.alpha, next_norm, self.eps, b["out"], b["rstd"],
                          b["xn_next"] if next_norm is not None else None, b["rstd_next"] if next_norm is not None else None, stream)
-        self._call = (r, y, gate, gate_rows, next_norm, made)
+        self._call = (r, y, gate, gate_rows, next_norm, made) if train else None
         return b["out"] if next_norm is None else (b["out"], b["xn_next"])
 
     __call__ = forward
@@ -590,7 +595,7 @@ class MoEBlock:
         fp32, or None), "dw_next" (of next_norm, or None), and "dw_in"; where xn was given to forward(), "dw_in" is None and "dxn"
         is xn's gradient, both of which the block before takes: a.backward(g["dr"], g["dxn"])."""
         if self._call is None:
-            raise RuntimeError("backward() follows a forward()")
+            raise RuntimeError("backward() follows a forward(train=True)")
         r, y, gate, gate_rows, next_norm, made = self._call
         b, f = self._buf, self.ffn
         T, d = r.shape

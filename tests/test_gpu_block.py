@@ -158,3 +158,23 @@ def test_block_with_few_tokens_and_a_gate_per_sequence():
         MoEBlock(ffn, gains[0], gains[1])(r, gate=gate, gate_rows=2)
     with pytest.raises(ValueError):
         MoEBlock(ffn, gains[0][:8], gains[1])
+
+
+def test_block_refuses_a_training_forward_on_its_own_outputs():
+    E, d, f, k = 4, 128, 64, 2
+    w = weights(E, d, f, seed=5)
+    gains = 1 + 0.1 * torch.randn(2, d, device="cuda")
+    block = MoEBlock(MoEFFN(w["w_router"], w["w_gateup"], w["w_down"], k, bias=w["bias"]), gains[0], gains[1])
+    r = torch.randn(9, d, device="cuda").bfloat16()
+    out, xn = block(r, next_norm=gains[1])
+    with pytest.raises(RuntimeError):
+        block.backward(r)  # nothing was kept
+    with pytest.raises(ValueError):
+        block(out, train=True)
+    with pytest.raises(ValueError):
+        block(r, xn=xn, next_norm=gains[1], train=True)
+    block(r, xn=xn, train=True)  # not overwritten without a next norm
+    block.backward(torch.ones_like(r))
+    first = block(r).clone()
+    again = block(block(r))  # without training the stream may be updated in place
+    assert torch.equal(again, block(first))
