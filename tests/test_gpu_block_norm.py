@@ -325,3 +325,26 @@ def test_refusals():
         N.block_norm_in_backward(st["dxn"], None, st["r"], st["w"], fwd["rstd"], torch.empty_like(st["r"]),
                                  torch.empty_like(st["w"]), ws)
     assert e.value.status == N.MOE_ERR_WORKSPACE
+
+
+def test_rows_past_two_to_the_31_elements():
+    """The last rows of a stream of more than 2^31 elements, against the formulas."""
+    d = 8192
+    T = 2 ** 31 // d + 5
+    g = torch.Generator(device="cuda").manual_seed(11)
+    y, dout = (torch.empty(T, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    w = 1 + 0.3 * torch.randn(d, device="cuda", generator=g)
+    xn, dr, dy = torch.empty_like(y), torch.empty_like(y), torch.empty_like(y)
+    rstd, dw = torch.empty(T, device="cuda"), torch.empty(d, device="cuda")
+    N.block_norm_in(y, w, EPS, xn, rstd)
+    ws = torch.empty(N.block_norm_backward_workspace_size(T, d), dtype=torch.uint8, device="cuda")
+    N.block_norm_out_backward(dout, None, y, None, w, None, 0, 0.5, None, rstd, None, dr, dy, dw, None, None, ws)
+    a = slice(T - 4, T)
+    y, dout, w, rs = y[a].double(), dout[a].double(), w.double(), f64_norm(y[a].double())
+    near(rstd[a], rs[:, 0], rs[:, 0], "rstd")
+    near(xn[a], y * rs * w, (y * rs * w).abs(), "xn")
+    near(dr[a], 0.5 * dout, 0.5 * dout.abs(), "dr")
+    rs = rstd[a].double()[:, None]
+    hat, dn = y * rs, dout * w
+    near(dy[a], rs * (dn - hat * (dn * hat).mean(1, keepdim=True)),
+         rs * (dn.abs() + hat.abs() * (dn * hat).abs().mean(1, keepdim=True)), "dy")
