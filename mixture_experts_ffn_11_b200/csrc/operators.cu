@@ -195,10 +195,50 @@ NormShape norm_shape(int T, int d, int sms, size_t row_bytes, int vpt1_max, int 
     return s;
 }
 
-template <typename... KArgs>
-cudaError_t norm_smem(void (*kernel)(KArgs...), size_t bytes) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Limits of the kernels' dynamic shared memory: the most that any ring takes, whatever the call, so that no call depends on another and no
+// thread lowers what another is about to use. (Without it the limit of 48 KB holds for static and dynamic memory together.)
+template <typename... Kernels>
+cudaError_t norm_ring_limit(Kernels... kernels) {
+    cudaError_t e = cudaSuccess;
+    ((e = e == cudaSuccess ? cudaFuncSetAttribute(kernels, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingBytes) : e), ...);
+    return e;
+}
+template <typename R, int VPT>
+cudaError_t norm_ring_limits() {
+    return norm_ring_limit(block_norm_in_kernel<R, VPT, true>, block_norm_out_kernel<R, VPT, false, true>,
+                           block_norm_out_kernel<R, VPT, true, true>, block_norm_in_grad_kernel<R, VPT, true>);
+}
+template <typename R, bool NEXT, bool GATE>
+cudaError_t norm_grad_ring_limits() {
+    return norm_ring_limit(block_norm_out_grad_kernel<R, NEXT, GATE, true, false>, block_norm_out_grad_kernel<R, NEXT, GATE, true, true>);
+}
+template <typename R>
+cudaError_t norm_ring_limits() {
+    cudaError_t e = norm_ring_limits<R, 1>();
+    if (e == cudaSuccess) e = norm_ring_limits<R, 2>();
+    if (e == cudaSuccess) e = norm_ring_limits<R, 4>();
+    if (e == cudaSuccess) e = norm_grad_ring_limits<R, false, false>();
+    if (e == cudaSuccess) e = norm_grad_ring_limits<R, false, true>();
+    if (e == cudaSuccess) e = norm_grad_ring_limits<R, true, false>();
+    if (e == cudaSuccess) e = norm_grad_ring_limits<R, true, true>();
+    return e;
+}
+
+// The device, with those limits set once.
+moe_status_t norm_device(DeviceInfo& di) {
+    moe_status_t st = device_info(di);
+    if (st != MOE_OK) return st;
+    static bool ready[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (e == cudaSuccess && !ready[dev]) {
+        e = norm_ring_limits<float>();
+        if (e == cudaSuccess) e = norm_ring_limits<__nv_bfloat16>();
+        ready[dev] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    return MOE_OK;
 }
 
 moe_status_t check_norm_sizes(int T, int d, moe_stream_type_t type) {
@@ -246,8 +286,6 @@ cudaError_t launch_norm_in(const void* x, const float* w, int T, int d, float ep
     const NormShape s = norm_shape(T, d, sms, (size_t)d * sizeof(R), 128, 4, 8);
     cudaError_t e = cudaSuccess;
 #define CALL(V, RING)                                                                                                      \
-    e = norm_smem(block_norm_in_kernel<R, V, RING>, s.smem);                                                               \
-    if (e == cudaSuccess)                                                                                                  \
     e = launch_pdl(block_norm_in_kernel<R, V, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream,                        \
                    reinterpret_cast<const R*>(x), w, T, d, eps, reinterpret_cast<__nv_bfloat16*>(xn), rstd, s.stages)
     MOE_NORM_CASES(s, CALL)
@@ -260,8 +298,6 @@ cudaError_t launch_norm_out(const NormOutArgs& a, int sms, cudaStream_t stream) 
     const NormShape s = norm_shape(a.T, a.d, sms, (size_t)a.d * (2 + sizeof(R) + (a.gate ? 2 : 0)), 128, 2, 8);
     cudaError_t e = cudaSuccess;
 #define CALL(V, RING)                                                                                                \
-    e = norm_smem(block_norm_out_kernel<R, V, NEXT, RING>, s.smem);                                                  \
-    if (e == cudaSuccess)                                                                                            \
     e = launch_pdl(block_norm_out_kernel<R, V, NEXT, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream, a, s.stages)
     MOE_NORM_CASES(s, CALL)
 #undef CALL
@@ -281,8 +317,6 @@ cudaError_t launch_norm_in_grad(const NormInGradArgs& a, int sms, cudaStream_t s
     B = s.grid;
     cudaError_t e = cudaSuccess;
 #define CALL(V, RING)                                                                                                    \
-    e = norm_smem(block_norm_in_grad_kernel<R, V, RING>, s.smem);                                                        \
-    if (e == cudaSuccess)                                                                                                \
     e = launch_pdl(block_norm_in_grad_kernel<R, V, RING>, dim3(s.grid), dim3(s.threads), s.smem, stream, a, s.stages)
     MOE_NORM_CASES(s, CALL)
 #undef CALL
@@ -346,9 +380,10 @@ cudaError_t launch_norm_out_grad(const NormOutGradArgs& a, int ctas, int sms, cu
         stages = (int)std::min<size_t>(BN_MAX_STAGES, (kNormRingBytes / per_sm - 1024) / row_bytes);
         cfg.dynamicSmemBytes = 128 + (size_t)stages * row_bytes;
         int resident = sms * per_sm;
-        cudaError_t e = norm_smem(ring, kNormRingBytes);
-        if (CLUSTER && e == cudaSuccess) e = resident_clusters(ring, ctas, kNormPairThreads, kNormPairBytes, resident);
-        if (e != cudaSuccess) return e;
+        if (CLUSTER) {
+            const cudaError_t e = resident_clusters(ring, ctas, kNormPairThreads, kNormPairBytes, resident);
+            if (e != cudaSuccess) return e;
+        }
         B = std::min(resident, a.T);
     }
     B = std::min(B, norm_grad_ctas(a.T, a.d));
@@ -522,7 +557,7 @@ moe_status_t moe_block_norm_in(const void* x, moe_stream_type_t type, const floa
     if (!w || (T > 0 && (!x || !xn || !rstd))) return fail(MOE_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(x) || !aligned16(w) || !aligned16(xn)) return fail(MOE_ERR_INVALID_ARG, "x, w and xn must be 16-byte aligned");
     DeviceInfo di;
-    if ((st = operator_device(di)) != MOE_OK) return st;
+    if ((st = norm_device(di)) != MOE_OK) return st;
     if (T == 0) return MOE_OK;
     return check_launch("block_norm_in", type == MOE_STREAM_FP32 ? launch_norm_in<float>(x, w, T, d, eps, xn, rstd, di.sms, stream)
                                                                  : launch_norm_in<__nv_bfloat16>(x, w, T, d, eps, xn, rstd, di.sms,
@@ -542,7 +577,7 @@ moe_status_t moe_block_norm_out(const moe_bf16_t* y, const void* r, moe_stream_t
         !aligned16(xn))
         return fail(MOE_ERR_INVALID_ARG, "y, r, w, gate, w_next, out and xn must be 16-byte aligned");
     DeviceInfo di;
-    if ((st = operator_device(di)) != MOE_OK) return st;
+    if ((st = norm_device(di)) != MOE_OK) return st;
     if (T == 0) return MOE_OK;
     const NormOutArgs a{reinterpret_cast<const __nv_bfloat16*>(y), r, w, reinterpret_cast<const __nv_bfloat16*>(gate), w_next, out,
                         rstd, reinterpret_cast<__nv_bfloat16*>(xn), rstd_next, T, d, gate_rows, alpha, eps};
@@ -573,7 +608,7 @@ moe_status_t moe_block_norm_in_backward(const moe_bf16_t* dxn, const void* dres,
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
     if (need && !aligned16(ws)) return fail(MOE_ERR_WORKSPACE, "workspace not 16-byte aligned");
     DeviceInfo di;
-    if ((st = operator_device(di)) != MOE_OK) return st;
+    if ((st = norm_device(di)) != MOE_OK) return st;
     if (T == 0) {  // no tokens: the gain's gradient is zero
         const cudaError_t e = cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)d, stream);
         return e == cudaSuccess ? MOE_OK : fail(MOE_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
@@ -610,7 +645,7 @@ moe_status_t moe_block_norm_out_backward(const void* dout, const moe_bf16_t* dxn
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
     if (need && !aligned16(ws)) return fail(MOE_ERR_WORKSPACE, "workspace not 16-byte aligned");
     DeviceInfo di;
-    if ((st = operator_device(di)) != MOE_OK) return st;
+    if ((st = norm_device(di)) != MOE_OK) return st;
     if (T == 0) {  // no tokens: the gains' gradients are zero
         cudaError_t e = cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)d, stream);
         if (e == cudaSuccess && dw_next) e = cudaMemsetAsync(dw_next, 0, sizeof(float) * (size_t)d, stream);
