@@ -401,8 +401,10 @@ moe_status_t moe_unpermute_combine(const moe_bf16_t* y_perm, const int32_t* inv_
  *   h_tj = bf16(w_tj * silu(x_t Wg_e^T) * (x_t Wu_e^T)), e = topk_idx[t][j]
  *   y_t  = bf16(sum_j Wd_e h_tj + Wd_shared bf16(silu(x_t Wg_s^T) * (x_t Wu_s^T)))
  * Every sum runs in an order fixed by the sizes and the routing: the same
- * inputs give the same bits. A token with NaN in it gives NaN in its own row
- * (its NaN logits count as the lowest, so its expert ids stay in range).
+ * inputs give the same bits. An infinity or NaN among an expert's weights
+ * reaches the tokens that chose this expert, and no others. A token with NaN
+ * in it gives NaN in its own row (its NaN logits count as the lowest, so its
+ * expert ids stay in range).
  *   x [T][d] bf16, w_router [E][d] fp32, bias [E] fp32 or NULL,
  *   w_gateup [E][2f][d], w_down [E][d][f] bf16 (as in the grouped GEMMs),
  *   w_gateup_shared [2fs][d], w_down_shared [d][fs] bf16, or NULL with fs = 0

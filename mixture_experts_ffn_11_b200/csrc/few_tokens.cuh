@@ -252,8 +252,41 @@ __device__ __forceinline__ bool grid_barrier(int* counter, int* s_flag) {
     return *s_flag != 0;
 }
 
+// One element of the down projection over the steps s0 .. s1 of its block of output columns, from the experts that the token chose
+// and no others: choice[a * pitch], as which of its k choices it has the active expert a (or -1).
+//
+// In the MMAs a token without the expert has zeros in its column, and zero times an infinity or NaN among that expert's weights is NaN
+// where the formula has no term at all. That always shows as a NaN in the sum (never as an infinity, nor as a wrong number), so a sum
+// that is NaN, and only that, is made again here: finite weights cost one comparison per output (0.2 us of 46). One thread, in order; a
+// token that holds NaN itself comes here with all its columns, which is slow and nothing more.
+__device__ __forceinline__ float few_down_of_chosen(const FewArgs& p, const int* active, int A, const int8_t* choice, int pitch, int t,
+                                                 int column, int s0, int s1) {
+    const int fsteps = (p.f + FT_KC - 1) / FT_KC;
+    float sum = 0.f;
+    for (int a = min(s0 / fsteps, A); a <= A; ++a) {
+        const int first = a * fsteps;  // the expert's first step; the shared one's run on to the block's end
+        if (first >= s1) break;
+        const int j = choice[a * pitch];
+        if (j < 0) continue;
+        const int K = a < A ? p.f : p.fs;
+        const int k0 = max(s0 - first, 0) * FT_KC, k1 = min((s1 - first) * FT_KC, K);
+        const __nv_bfloat16* w = (a < A ? p.w_down + (size_t)active[a] * p.d * p.f : p.s_down) + (size_t)column * K;
+        const __nv_bfloat16* h = p.h + (size_t)(a < A ? t * p.k + j : p.T * p.k + t) * p.ldh;
+        for (int k = k0; k < k1; k += 8) {
+            const uint4 wv = *reinterpret_cast<const uint4*>(w + k), hv = __ldcg(reinterpret_cast<const uint4*>(h + k));
+            const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w}, hu[4] = {hv.x, hv.y, hv.z, hv.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack_bf16x2(wu[i]), y = unpack_bf16x2(hu[i]);
+                sum = fmaf(x.y, y.y, fmaf(x.x, y.x, sum));
+            }
+        }
+    }
+    return sum;
+}
+
 template <int NT>
-__global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs p) {
+__global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const __grid_constant__ FewArgs p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     using S = FewShape<NT>;
     constexpr int STAGES = S::STAGES, RB = S::RB, SLOT_BYTES = FT_THREADS * 16, STAGE_BYTES = (4 + NT) * SLOT_BYTES;
@@ -588,6 +621,7 @@ __global__ void __launch_bounds__(FT_THREADS, 1) few_tokens_kernel(const FewArgs
                     float v = 0.f;
 #pragma unroll
                     for (int q = 0; q < FT_WARPS; ++q) v += element(q, col >> 4, t >> 3, col & 15, t & 7);
+                    if (v != v) v = few_down_of_chosen(p, s_active, A, s_choice + t, 8 * NT, t, cb * 32 + c, begin - cb * per, end - cb * per);
                     if (whole)
                         p.y[(size_t)t * p.d + cb * 32 + c] = __float2bfloat16_rn(v);
                     else
