@@ -688,9 +688,11 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
     };
     // its gradients, from the sums over all columns
     const auto finish = [&](Row& q, int t, float rs, float rn, const float (&s)[3]) {
-        float c = 0.f;  // dR = dout + rstd' dxn w' - c out
-        if constexpr (NEXT) c = rn * rn * rn * s[1] * inv_d;
-        const float mean = (NEXT ? s[0] - c * s[2] : s[0]) * inv_d;
+        // dR = dout + rstd' (dxn w' - c out), S2 = SA - rstd' c SB. Factors in an order that keeps the products of rstd' and of out near 1
+        // (rstd'^3 alone leaves fp32's range for rows of rms 1e-13 or 1e15)
+        float c = 0.f;
+        if constexpr (NEXT) c = rn * (rn * s[1] * inv_d);
+        const float mean = (NEXT ? s[0] - rn * (c * s[2]) : s[0]) * inv_d;
         if (!mine) return;
         q.up.keep_packed();
         q.y.keep_packed();
@@ -705,7 +707,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint64_t dR = fu[i];
-            if constexpr (NEXT) dR = fma2(minus_c, fo[i], fma2(mul2(rn2, gn[i]), fd[i], dR));
+            if constexpr (NEXT) dR = fma2(rn2, fma2(minus_c, fo[i], mul2(gn[i], fd[i])), dR);
             const uint64_t hat = mul2(fy[i], rs2), e = mul2(dR, hat);
             uint64_t dn = mul2(dR, g[i]);
             if constexpr (GATE) {
