@@ -621,9 +621,10 @@ moe_status_t moe_set_gemm_kernel(moe_gemm_kernel_t kind);
  * the current device, the wait limit in nanoseconds (0 restores the default
  * of 2 s) and, with stall != 0, makes the MMA-issuing warp of every bf16 and
  * e4m3 grouped GEMM first wait on a barrier that nothing arrives on, and the
- * barrier inside moe_few_tokens wait for one arrival too many, so that a
- * test can run the timeout path on purpose. It synchronises the device first.
- * Results of GEMMs launched while stall is set are undefined; the device
+ * barrier inside moe_few_tokens wait for one arrival too many, and the block
+ * norms that take many rows or wide ones wait likewise, so that a test can run
+ * the timeout path on purpose. It synchronises the device first.
+ * Results of kernels launched while stall is set are undefined; the device
  * error word reports the timeout. Not for normal use. */
 moe_status_t moe_test_set_wait(unsigned long long limit_ns, int stall);
 

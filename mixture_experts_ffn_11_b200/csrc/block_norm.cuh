@@ -118,17 +118,18 @@ struct RowArray {
 // of arrays issues one array's copy, else thread 0 all of them (which of the two is
 // faster was measured kernel by kernel: 4096 rows of 8192 in fp32 in two CTAs 192 us by one thread, 147 us spread; 8192 rows of 4096 in
 // bf16 in one CTA 94 and 103 us).
+//
+// When a wait runs out, no row is copied any more, and what is under way is waited for before the CTA leaves. The warps of a SPREAD ring
+// have to agree on which row is the first that is not copied (its barrier counts all their copies): thread 0 decides, in advance(),
+// and leaves the decision for the others to read behind the barrier that every row has between its advance() and its release().
 template <bool RING, int NARR, bool SPREAD = false>
 struct RowRing {
     RowArray arr[NARR];
     uint64_t* full;
-    volatile int* abort_flag;
-    uint8_t* data;
     int cols, col0, n;  // columns of the arrays, the first one taken, how many
     uint32_t row_bytes;
     int stages, stage, step, end, next;  // next: the row to copy next
     uint32_t phase;
-    uint64_t limit;
     int row;
 
     // columns c0 .. c0 + n_cols of d, rows first, first + step, ... < end
@@ -142,30 +143,36 @@ struct RowRing {
         next = first;
         if constexpr (RING) {
             full = reinterpret_cast<uint64_t*>(smem);
-            abort_flag = reinterpret_cast<volatile int*>(full + BN_MAX_STAGES);
-            data = smem + 128;
             stages = n_stages;
             stage = -1;
             phase = 1;
-            limit = wait_limit_ns();
             row_bytes = 0;
 #pragma unroll
             for (int i = 0; i < NARR; ++i) row_bytes += (uint32_t)(n * arr[i].size);
             if (threadIdx.x == 0) {
                 for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
-                *abort_flag = 0;
+                mbar_init(never(), 1);
+                *abort_flag() = 0;
+                *limit() = wait_limit_ns();
                 fence_mbar_init();
             }
             __syncthreads();
-            for (int s = 0; s < stages; ++s) copy(s);
+            for (int s = 0; s < stages; ++s) copy(s, false);
+            // (the test hook moe_test_set_wait: a wait that nothing ends)
+            if (*reinterpret_cast<volatile int*>(&g_wait_stall) != 0) mbar_wait_within(never(), 0, abort_flag(), limit());
         }
     }
-    __device__ __forceinline__ void copy(int s) {  // the next row into stage s
-        if (next >= end || *abort_flag) return;
+    // [3]: raised when a wait ran out; thread 0's decisions for even and odd rows (SPREAD, consecutive rows)
+    __device__ __forceinline__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(full + BN_MAX_STAGES); }
+    __device__ __forceinline__ uint8_t* data() const { return reinterpret_cast<uint8_t*>(full) + 128; }
+    __device__ __forceinline__ volatile uint64_t* limit() const { return full + BN_MAX_STAGES + 3; }
+    __device__ __forceinline__ uint64_t* never() const { return full + BN_MAX_STAGES + 2; }  // a barrier that nothing arrives on
+    __device__ __forceinline__ void copy(int s, bool stopped) {  // the next row into stage s
+        if (next >= end || stopped) return;
         const int warp = threadIdx.x >> 5;
         if (SPREAD ? (threadIdx.x & 31) == 0 : threadIdx.x == 0) {
             if (warp == 0) mbar_arrive_expect_tx(&full[s], row_bytes);
-            uint8_t* to = data + (size_t)s * row_bytes;
+            uint8_t* to = data() + (size_t)s * row_bytes;
 #pragma unroll
             for (int i = 0; i < NARR; ++i) {
                 const uint32_t bytes = (uint32_t)(n * arr[i].size);
@@ -186,13 +193,20 @@ struct RowRing {
         if constexpr (RING) {
             if (++stage == stages) stage = 0;
             if (stage == 0) phase ^= 1u;
-            if (!mbar_wait_within(&full[stage], phase, abort_flag, limit) && threadIdx.x == 0 && row < next)
+            if (!mbar_wait_within(&full[stage], phase, abort_flag(), limit()) && threadIdx.x == 0 && row < next)
                 mbar_wait_drain(&full[stage], phase);  // no copy is in flight when the CTA leaves
+            if (SPREAD && threadIdx.x == 0) abort_flag()[1 + (row & 1)] = *abort_flag();
         }
         return true;
     }
     // Where the current row lies, for get() and release() now or some rows later (until it is released)
     __device__ __forceinline__ int here() const { return RING ? stage : row; }
+    // Where the row `back` rows before that one lies (back at most 2 and below the number of stages)
+    __device__ __forceinline__ int here_before(int back) const {
+        if constexpr (!RING) return row - back;
+        const int s = stage - back;
+        return s < 0 ? s + stages : s;
+    }
     // Elements of array i of the current row, or of the row that was at `at`
     template <typename E>
     __device__ __forceinline__ const E* get(int i) const {
@@ -205,7 +219,7 @@ struct RowRing {
 #pragma unroll
             for (int j = 0; j < NARR; ++j)
                 if (j < i) at += (uint32_t)(n * arr[j].size);
-            return reinterpret_cast<const E*>(data + (size_t)at_row * row_bytes + at);
+            return reinterpret_cast<const E*>(data() + (size_t)at_row * row_bytes + at);
         } else {
             const int r = arr[i].per > 1 ? at_row / arr[i].per : at_row;
             return reinterpret_cast<const E*>(reinterpret_cast<const uint8_t*>(arr[i].base) + ((size_t)r * cols + col0) * arr[i].size);
@@ -215,7 +229,7 @@ struct RowRing {
     __device__ __forceinline__ void release() { release(here()); }
     __device__ __forceinline__ void release(int at_row) {
         if constexpr (RING) {
-            copy(at_row);
+            copy(at_row, abort_flag()[SPREAD ? 1 + (row & 1) : 0] != 0);
         }
     }
 };
@@ -259,16 +273,22 @@ __device__ __forceinline__ void block_sums(float (&v)[3], float* red) {
 // Rows wider than a CTA's threads hold are cut by columns over the CTAs of a cluster. Each sends its sums of a row to all of them (st.async
 // into shared memory, counted by the receiver's barrier) and adds what it got in the order of the CTAs, one row later: about 1 us on
 // the way, in which the CTA takes up the next row. Four slots: a CTA sends row m only with every other's sums of row m - 2,
-// which that one sends once all its threads have taken those of row m - 4.
+// which that one sends once all its threads have taken those of row m - 4. A CTA whose wait ran out sends no more and expects no
+// more (its barrier may still be waiting for an earlier row); the others' waits then run out too.
 struct ClusterSums {
     float4 slot[4][BN_MAX_CLUSTER];
     uint64_t bar[4];
+    uint64_t limit;
+    uint32_t expect;  // bytes of a row
     int abort_flag;
 };
-__device__ __forceinline__ void cluster_sums_init(ClusterSums& x) {
+__device__ __forceinline__ void cluster_sums_init(ClusterSums& x, uint32_t ctas) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) mbar_init(&x.bar[i], 1);
+        // (the test hook moe_test_set_wait: one CTA's sums more than there are)
+        x.expect = (ctas + (*reinterpret_cast<volatile int*>(&g_wait_stall) != 0 ? 1u : 0u)) * 16u;
         x.abort_flag = 0;
+        x.limit = wait_limit_ns();
         fence_mbar_init();
     }
     cluster_sync();
@@ -277,14 +297,15 @@ __device__ __forceinline__ void cluster_sums_init(ClusterSums& x) {
 __device__ __forceinline__ void cluster_sums_send(ClusterSums& x, int n, uint32_t ctas, uint32_t rank, const float (&v)[3]) {
     const int turn = n & 3;
     const int i = (int)threadIdx.x - (int)blockDim.x + 32;  // the last warp
-    if (i == 0) mbar_arrive_expect_tx(&x.bar[turn], ctas * 16u);
-    if (i >= 0 && i < (int)ctas)
+    if (i < 0 || *reinterpret_cast<volatile int*>(&x.abort_flag)) return;
+    if (i == 0) mbar_arrive_expect_tx(&x.bar[turn], x.expect);
+    if (i < (int)ctas)
         store_remote(mapa_shared(smem_u32(&x.slot[turn][rank]), i), make_float4(v[0], v[1], v[2], 0.f),
                      mapa_shared(smem_u32(&x.bar[turn]), i));
 }
-__device__ __forceinline__ void cluster_sums_take(ClusterSums& x, int n, uint32_t ctas, uint64_t limit, float (&v)[3]) {
+__device__ __forceinline__ void cluster_sums_take(ClusterSums& x, int n, uint32_t ctas, float (&v)[3]) {
     const int turn = n & 3;
-    mbar_wait_within(&x.bar[turn], (uint32_t)(n >> 2) & 1u, &x.abort_flag, limit);
+    mbar_wait_within(&x.bar[turn], (uint32_t)(n >> 2) & 1u, &x.abort_flag, static_cast<const volatile uint64_t*>(&x.limit));
     v[0] = v[1] = v[2] = 0.f;
     for (uint32_t r = 0; r < ctas; ++r) {
         const float4 q = x.slot[turn][r];
@@ -621,11 +642,7 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
     grid_dep_wait();
     grid_dep_trigger();
     rows.start(smem, stages, a.d, c0, nvec * 8, t0, 1, t1);
-    uint64_t limit = 0;
-    if constexpr (CLUSTER) {
-        limit = wait_limit_ns();
-        cluster_sums_init(across);
-    }
+    if constexpr (CLUSTER) cluster_sums_init(across, ctas);
     // two columns to an operation throughout (fp32 pairs): a row's instructions weigh as much as its bytes
     uint64_t g[4], gn[4], acc[4], acc_next[4], acc_gate[4];
     load_gains(a.w + c0, nvec, g);
@@ -751,7 +768,6 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
             finish(q, t, rs, rn, s);
         }
     } else {
-        int before = 0, before2 = 0;  // where the two rows before lie
         float rs_before = 0.f, rn_before = 0.f;
         for (int n = 0;; ++n) {
             const bool more = rows.advance();
@@ -762,15 +778,14 @@ __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(con
                 load(q, rows.here());
                 sums(q, rs, rn, n, s);
                 cluster_sums_send(across, n, ctas, rank, s);
-                if (n > 1) rows.release(before2);
+                if (n > 1) rows.release(rows.here_before(2));
             }
             if (n > 0) {
-                load(q, before);
-                cluster_sums_take(across, n - 1, ctas, limit, s);
+                load(q, RING && !more ? rows.here() : rows.here_before(1));  // (behind the last row the ring has not moved)
+                cluster_sums_take(across, n - 1, ctas, s);
                 finish(q, t0 + n - 1, rs_before, rn_before, s);
             }
             if (!more) break;
-            before2 = before, before = rows.here();
             rs_before = rs, rn_before = rn;
         }
     }

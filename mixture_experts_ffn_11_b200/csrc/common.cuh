@@ -19,8 +19,9 @@ __device__ __forceinline__ void flag_error(unsigned int bit) { atomicOr(&g_devic
 // shorten it (moe_test_set_wait); kernels read it when a wait does not succeed at once.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 __device__ unsigned long long g_wait_limit_ns = kWaitLimitNs;
-// Test hook (moe_test_set_wait): when non-zero, the MMA-issuing warp of each bf16 grouped GEMM first waits on a
-// barrier that nothing arrives on, so the bounded wait runs out and the kernel takes its abort path.
+// Test hook (moe_test_set_wait): when non-zero, the MMA-issuing warp of each bf16 or e4m3 grouped GEMM first waits on a
+// barrier that nothing arrives on, so the bounded wait runs out and the kernel takes its abort path; the few-token layer's
+// and the block norms' waits take it likewise.
 __device__ int g_wait_stall = 0;
 
 __device__ __forceinline__ uint64_t wait_limit_ns() { return *reinterpret_cast<volatile unsigned long long*>(&g_wait_limit_ns); }

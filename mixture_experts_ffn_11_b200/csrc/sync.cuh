@@ -65,15 +65,19 @@ __device__ __forceinline__ void store_remote(uint32_t cluster_addr, const float4
 
 // As mbar_wait_bounded, for waits once per K block on several roles' critical paths: the limit is the caller's (read once, by
 // wait_limit_ns() at the kernel's start; reading it in the wait costs an L2 access each time the barrier is not ready), the clock
-// is looked at only after a first poll, and each poll sleeps in hardware for up to 20 us instead of spinning.
-__device__ __forceinline__ bool mbar_wait_within(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit) {
+// is looked at only after a first poll, and each poll sleeps in hardware for up to 20 us instead of spinning. The limit is a value, or
+// where it lies in shared memory (for kernels that have no two registers for it).
+__device__ __forceinline__ uint64_t limit_of(uint64_t limit) { return limit; }
+__device__ __forceinline__ uint64_t limit_of(const volatile uint64_t* limit) { return *limit; }
+template <typename Limit>
+__device__ __forceinline__ bool mbar_wait_within(uint64_t* bar, uint32_t parity, volatile int* abort_flag, Limit limit) {
     const uint32_t addr = smem_u32(bar);
     if (mbar_try_wait_for(addr, parity, 20000)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
         if (mbar_try_wait_for(addr, parity, 20000)) return true;
         if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > limit) {
+        if (globaltimer_ns() - t0 > limit_of(limit)) {
             *abort_flag = 1;
             flag_error(MOE_DEVERR_WAIT_TIMEOUT);
             return false;
