@@ -50,6 +50,19 @@ def _encode_fp8(w, halves: int):
     return q, s
 
 
+def _in_use(buffers: dict, stream, seen: set):
+    """Tell the caching allocator that `stream` uses these buffers, which were allocated on whichever stream was current: when they are
+    dropped (for another number of tokens), their memory is not given out while that stream's work is still to come. `seen`: streams
+    it has been told of."""
+    if stream.cuda_stream in seen:
+        return
+    seen.add(stream.cuda_stream)
+    for v in buffers.values():
+        for t in v if isinstance(v, tuple) else (v,):  # (encoded rows: values and scales)
+            if t is not None:
+                t.record_stream(stream)
+
+
 class MoEFFN:
     """One MoE feed-forward layer with packed expert weights.
 
@@ -196,7 +209,7 @@ class MoEFFN:
             b["xq"], b["hq"] = rows(R, d), rows(R, f)
             if self.shared_f:
                 b["xq_shared"], b["hq_shared"] = rows(T, d), rows(T, self.shared_f)
-        self.buf, self._T = b, T
+        self.buf, self._T, self._seen = b, T, set()
         return b
 
     def forward(self, x, stream=None, timing=None, train: bool = False):
@@ -213,6 +226,12 @@ class MoEFFN:
         T = x.shape[0]
         b = self.buffers(T)
         s = stream if stream is not None else torch.cuda.current_stream(x.device)
+        few = self._few(T) and not train
+        if few and "few_ws" not in b:
+            n = N.few_tokens_workspace_size(T, self.d, self.f, self.shared_f, self.E, self.k)
+            b["few_ws"] = torch.empty(n, dtype=torch.uint8, device=self.device)
+            self._seen = set()
+        _in_use(b, s, self._seen)
         self._x = x  # the backward pass reads the forward's input and intermediates
 
         def mark(name, first):
@@ -222,10 +241,7 @@ class MoEFFN:
                 timing[name] = (torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
             timing[name][0 if first else 1].record(s)
 
-        if self._few(T) and not train:
-            if "few_ws" not in b:
-                n = N.few_tokens_workspace_size(T, self.d, self.f, self.shared_f, self.E, self.k)
-                b["few_ws"] = torch.empty(n, dtype=torch.uint8, device=self.device)
+        if few:
             mark("few", True)
             N.few_tokens(x, self.w_router, self.bias, self.w_gateup, self.w_down, self.w_gateup_shared, self.w_down_shared,
                          self.k, self.route, b["logits"], b["topk_idx"], b["topk_w"], b["y"], b["few_ws"], s)
@@ -282,7 +298,9 @@ class MoEFFN:
         if fused:
             N.grouped_gemm_gateup_gather(x, b["perm_src"], self.w_gateup, b["offsets"], b["h"], None, s)
         elif save:
-            N.grouped_gemm_gateup_save(b["x_perm"], self.w_gateup, b["offsets"], b["h"], self._grad_buffers(T)["gu"], s)
+            g = self._grad_buffers(T)
+            _in_use(g, s, self._gseen)
+            N.grouped_gemm_gateup_save(b["x_perm"], self.w_gateup, b["offsets"], b["h"], g["gu"], s)
             self._gu_saved = True
         else:
             self.routed_gateup(b, s)
@@ -415,7 +433,7 @@ class MoEFFN:
             wsz = max(wsz, N.grouped_weight_grad_workspace_size(max(T, 1), 1, d, fs),
                       N.grouped_weight_grad_workspace_size(max(T, 1), 1, 2 * fs, d))
         g["wgrad_ws"] = torch.empty(max(wsz, 256), dtype=torch.uint8, device=dev)
-        self._gbuf, self._gT = g, T
+        self._gbuf, self._gT, self._gseen = g, T, set()
         return g
 
     def backward(self, dy, stream=None, weight_grads: bool = True, timing=None) -> dict:
@@ -434,6 +452,8 @@ class MoEFFN:
         b = self.buf
         wt = self._transposed()
         g = self._grad_buffers(T)
+        _in_use(b, s, self._seen)
+        _in_use(g, s, self._gseen)
         x = self._x
 
         def mark(name, first):
@@ -559,7 +579,7 @@ class MoEBlock:
             new = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=dev)  # noqa: E731
             self._buf = {"xn": new(T, d, t=torch.bfloat16), "rstd_in": new(T), "out": new(T, d, t=dtype), "rstd": new(T),
                          "xn_next": new(T, d, t=torch.bfloat16), "rstd_next": new(T)}
-            self._key = (T, dtype)
+            self._key, self._seen = (T, dtype), set()
         return self._buf
 
     def forward(self, r, xn=None, next_norm=None, gate=None, gate_rows: int = 0, train: bool = False, stream=None):
@@ -569,6 +589,8 @@ class MoEBlock:
         not be this block's own outputs, which the call overwrites."""
         T = r.shape[0]
         b = self._buffers(T, r.dtype)
+        stream = stream if stream is not None else torch.cuda.current_stream(self.ffn.device)
+        _in_use(b, stream, self._seen)
         if train and T > 0:
             store = lambda t: t.untyped_storage().data_ptr()  # noqa: E731
             if store(r) == store(b["out"]) or (xn is not None and next_norm is not None and store(xn) == store(b["xn_next"])):
@@ -606,8 +628,11 @@ class MoEBlock:
             self._gbuf = {"dr": new(T, d, t=r.dtype), "dy": new(T, d, t=torch.bfloat16), "dw_out": new(d), "dw_in": new(d),
                           "dw_next": new(d), "dgate": new(-(-T // gate_rows), d) if gate_rows else None,
                           "ws": new(max(ws, 16), t=torch.uint8)}
-            self._gkey = key
+            self._gkey, self._gseen = key, set()
         g = self._gbuf
+        stream = stream if stream is not None else torch.cuda.current_stream(f.device)
+        _in_use(b, stream, self._seen)
+        _in_use(g, stream, self._gseen)
         nxt = next_norm is not None
         N.block_norm_out_backward(dout, dxn, y, b["out"] if nxt else None, self.w_out, gate, gate_rows, self.alpha, next_norm,
                                   b["rstd"], b["rstd_next"] if nxt else None, g["dr"], g["dy"], g["dw_out"], g["dgate"],
