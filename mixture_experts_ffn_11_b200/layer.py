@@ -586,14 +586,18 @@ class MoEBlock:
         """The block's output stream [T, d] (a buffer of the block), or with next_norm (the next block's w_in) the pair (output
         stream, its normed input for the next block). xn: this block's normed input, if the block before made it. gate [ceil(T /
         gate_rows), d] bf16: a gate for this call, one row per gate_rows tokens. train: keep what backward() reads; r and xn then may
-        not be this block's own outputs, which the call overwrites."""
+        not be this block's own outputs, which the call overwrites. r may never be the MoEFFN's own output, nor xn with train."""
         T = r.shape[0]
         b = self._buffers(T, r.dtype)
         stream = stream if stream is not None else torch.cuda.current_stream(self.ffn.device)
         _in_use(b, stream, self._seen)
-        if train and T > 0:
+        if T > 0:
             store = lambda t: t.untyped_storage().data_ptr()  # noqa: E731
-            if store(r) == store(b["out"]) or (xn is not None and next_norm is not None and store(xn) == store(b["xn_next"])):
+            reads = {store(t) for t in ((r, xn) if train else (r,)) if t is not None}
+            y = getattr(self.ffn, "buf", {}).get("y")
+            if y is not None and store(y) in reads:
+                raise ValueError("r (and xn, with train) may not be the MoEFFN's own output: its forward() overwrites that before it is read")
+            if train and reads & {store(t) for t in (b["out"], b["xn_next"] if next_norm is not None else b["out"])}:
                 raise ValueError("backward() reads r and xn, and this forward would overwrite them: they are the block's own outputs")
         if gate is None and self.gate is not None:
             gate, gate_rows = self.gate.view(1, -1)[:min(T, 1)], max(T, 1)

@@ -1,0 +1,67 @@
+"""MoEBlock's checks on the host, on the CPU with a stand-in for the layer and the norms: calls whose inputs it would overwrite before it, or
+its backward pass, has read them, and backward passes whose kept values are gone."""
+import pytest
+import torch
+
+
+class Stream:
+    cuda_stream = 1
+
+
+@pytest.fixture
+def block(monkeypatch):
+    from mixture_experts_ffn_11_b200 import MoEBlock, layer
+
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    refuse = []
+
+    def norm_out(*args):
+        if refuse:
+            raise ValueError("refused")
+
+    monkeypatch.setattr(layer.N, "block_norm_out", norm_out)
+    for name in ("block_norm_in", "block_norm_in_backward", "block_norm_out_backward"):
+        monkeypatch.setattr(layer.N, name, lambda *a: None)
+
+    class FFN:
+        d, device, buf, _x = 16, torch.device("cpu"), {}, None
+
+        def forward(self, x, stream=None, train=False):
+            self._x = x
+            if self.buf.get("y") is None or self.buf["y"].shape != x.shape:
+                self.buf = {"y": torch.zeros(x.shape, dtype=torch.bfloat16)}
+            return self.buf["y"]
+
+        def backward(self, dy, weight_grads=True, stream=None):
+            return {"dx": torch.zeros_like(dy)}
+
+    made = MoEBlock(FFN(), torch.ones(16), torch.ones(16))
+    made.refuse = refuse
+    return made
+
+
+GAIN = torch.ones(16)
+
+
+def test_own_outputs_are_refused_where_the_backward_pass_reads_them(block):
+    r = torch.zeros(4, 16, dtype=torch.bfloat16)
+    out, nxt = block.forward(r, next_norm=GAIN, stream=Stream)
+    for change in ({"r": out}, {"r": out[:, :]}, {"xn": out}, {"r": nxt}, {"xn": nxt}):
+        with pytest.raises(ValueError):
+            block.forward(**{"r": r, "next_norm": GAIN, "train": True, "stream": Stream, **change})
+    for change in ({"r": out}, {"xn": out}, {"r": nxt}, {"xn": nxt}):  # without a backward pass all of them may be updated
+        block.forward(**{"r": r, "next_norm": GAIN, "stream": Stream, **change})
+    block.forward(nxt, train=True, stream=Stream)  # not written without a next norm
+    block.forward(r, xn=nxt, train=True, stream=Stream)
+
+
+def test_the_layers_output_is_refused_as_the_stream(block):
+    y = block.ffn.forward(torch.zeros(4, 16, dtype=torch.bfloat16))
+    for train in (False, True):
+        with pytest.raises(ValueError):
+            block.forward(y, train=train, stream=Stream)
+    r = torch.zeros(4, 16)
+    with pytest.raises(ValueError):
+        block.forward(r, xn=y, train=True, stream=Stream)
+    block.forward(r, xn=y, stream=Stream)
+    block.forward(y.clone(), train=True, stream=Stream)
