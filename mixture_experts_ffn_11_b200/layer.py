@@ -588,6 +588,7 @@ class MoEBlock:
         gate_rows), d] bf16: a gate for this call, one row per gate_rows tokens. train: keep what backward() reads; r and xn then may
         not be this block's own outputs, which the call overwrites. r may never be the MoEFFN's own output, nor xn with train."""
         T = r.shape[0]
+        self._call = None  # whatever becomes of this call, the kept values of the one before are gone
         b = self._buffers(T, r.dtype)
         stream = stream if stream is not None else torch.cuda.current_stream(self.ffn.device)
         _in_use(b, stream, self._seen)
@@ -608,7 +609,8 @@ class MoEBlock:
         y = self.ffn.forward(xn, stream, train=train)
         N.block_norm_out(y, r, self.w_out, gate, gate_rows, self.alpha, next_norm, self.eps, b["out"], b["rstd"],
                          b["xn_next"] if next_norm is not None else None, b["rstd_next"] if next_norm is not None else None, stream)
-        self._call = (r, y, gate, gate_rows, next_norm, made) if train else None
+        if train:
+            self._call = (r, xn, y, gate, gate_rows, next_norm, made)
         return b["out"] if next_norm is None else (b["out"], b["xn_next"])
 
     __call__ = forward
@@ -622,8 +624,11 @@ class MoEBlock:
         is xn's gradient, both of which the block before takes: a.backward(g["dr"], g["dxn"])."""
         if self._call is None:
             raise RuntimeError("backward() follows a forward(train=True)")
-        r, y, gate, gate_rows, next_norm, made = self._call
+        r, xn, y, gate, gate_rows, next_norm, made = self._call
         b, f = self._buf, self.ffn
+        if f._x is not xn:
+            raise RuntimeError("the MoEFFN has run another forward() since: its intermediates are gone (blocks in flight at once, or calls "
+                               "beside them, need a MoEFFN of their own: sibling() gives one over the same weights)")
         T, d = r.shape
         key = (T, r.dtype, gate_rows)
         if getattr(self, "_gkey", None) != key:

@@ -65,3 +65,31 @@ def test_the_layers_output_is_refused_as_the_stream(block):
         block.forward(r, xn=y, train=True, stream=Stream)
     block.forward(r, xn=y, stream=Stream)
     block.forward(y.clone(), train=True, stream=Stream)
+
+
+def test_backward_after_another_forward_of_the_layer(block):
+    r, dout = torch.zeros(4, 16), torch.zeros(4, 16)
+    block.forward(r, train=True, stream=Stream)
+    block.backward(dout, stream=Stream)
+    block.backward(dout, stream=Stream)
+    block.ffn.forward(torch.zeros(4, 16, dtype=torch.bfloat16))
+    with pytest.raises(RuntimeError):
+        block.backward(dout, stream=Stream)
+    from mixture_experts_ffn_11_b200 import MoEBlock
+
+    twin = MoEBlock(block.ffn, GAIN, GAIN)  # two blocks over one layer
+    block.forward(r, train=True, stream=Stream)
+    twin.forward(r, train=True, stream=Stream)
+    twin.backward(dout, stream=Stream)
+    with pytest.raises(RuntimeError):
+        block.backward(dout, stream=Stream)
+
+
+def test_a_refused_forward_leaves_nothing_to_go_back_to(block):
+    r, dout = torch.zeros(4, 16), torch.zeros(4, 16)
+    block.forward(r, train=True, stream=Stream)
+    block.refuse.append(True)  # the norms have overwritten what was kept by the time a later argument is refused
+    with pytest.raises(ValueError):
+        block.forward(r, train=True, stream=Stream)
+    with pytest.raises(RuntimeError):
+        block.backward(dout, stream=Stream)

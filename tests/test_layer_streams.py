@@ -22,6 +22,7 @@ def test_block_buffers_are_recorded_on_every_stream_once(monkeypatch):
         d, device = 16, torch.device("cpu")
 
         def forward(self, xn, stream=None, train=False):
+            self._x = xn
             return torch.zeros(xn.shape, dtype=torch.bfloat16)
 
         def backward(self, dy, weight_grads=True, stream=None):
