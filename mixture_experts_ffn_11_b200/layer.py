@@ -212,6 +212,14 @@ class MoEFFN:
         self.buf, self._T, self._seen = b, T, set()
         return b
 
+    @staticmethod
+    def _made_on(stream, there: bool, make, *args):
+        """make(*args), on `stream` unless it is there already: some buffers have first values, and the transposed weights are copies."""
+        if there:
+            return make(*args)
+        with torch.cuda.stream(stream):
+            return make(*args)
+
     def forward(self, x, stream=None, timing=None, train: bool = False):
         """y = MoE(x) for x [T, d] bf16 on the GPU. Returns the layer's output buffer [T, d] (bf16).
 
@@ -224,8 +232,8 @@ class MoEFFN:
         GEMMs (MXFP4), the copy of its rows; "few" alone, the whole layer, where the few-token kernels run).
         """
         T = x.shape[0]
-        b = self.buffers(T)
         s = stream if stream is not None else torch.cuda.current_stream(x.device)
+        b = self._made_on(s, self._T == T, self.buffers, T)
         few = self._few(T) and not train
         if few and "few_ws" not in b:
             n = N.few_tokens_workspace_size(T, self.d, self.f, self.shared_f, self.E, self.k)
@@ -298,7 +306,7 @@ class MoEFFN:
         if fused:
             N.grouped_gemm_gateup_gather(x, b["perm_src"], self.w_gateup, b["offsets"], b["h"], None, s)
         elif save:
-            g = self._grad_buffers(T)
+            g = self._made_on(s, getattr(self, "_gT", None) == T, self._grad_buffers, T)
             _in_use(g, s, self._gseen)
             N.grouped_gemm_gateup_save(b["x_perm"], self.w_gateup, b["offsets"], b["h"], g["gu"], s)
             self._gu_saved = True
@@ -450,8 +458,8 @@ class MoEFFN:
             raise RuntimeError("backward() follows a forward() over the same tokens")
         s = stream if stream is not None else torch.cuda.current_stream(dy.device)
         b = self.buf
-        wt = self._transposed()
-        g = self._grad_buffers(T)
+        wt = self._made_on(s, getattr(self, "_wt", None) is not None, self._transposed)
+        g = self._made_on(s, getattr(self, "_gT", None) == T, self._grad_buffers, T)
         _in_use(b, s, self._seen)
         _in_use(g, s, self._gseen)
         x = self._x

@@ -77,3 +77,36 @@ def test_buffers_outlive_the_work_of_another_stream(few, weights):
         assert torch.equal(got, want) and torch.equal(got_other, wanted)
         del filled
     assert N.get_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("weights,fs", [("bf16", 0), ("bf16", 128), ("mxfp4", 256), ("fp8", 128)])
+def test_first_call_on_a_side_stream_beside_a_busy_current_one(weights, fs):
+    """What a first call lays out (offsets of the shared expert, unit weights and transposed copies of the backward pass) is ready on the
+    stream of the call, whatever the current one has still to do."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mixture_experts_ffn_11_b200 import MoEFFN
+    from mixture_experts_ffn_11_b200 import _native as N
+
+    torch.cuda.set_device(0)
+    E, d, f, k, T = 16, 256, 256, 2, 24
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=g) * 0.05  # noqa: E731
+    args = (n(E, d), n(E, 2 * f, d).bfloat16(), n(E, d, f).bfloat16(), k, "topk_softmax", None,
+            n(2 * fs, d).bfloat16() if fs else None, n(d, fs).bfloat16() if fs else None)
+    first, again = (MoEFFN(*args, weights=weights) for _ in range(2))
+    train = weights == "bf16"
+    x, dy = torch.randn(T, d, device="cuda", generator=g).bfloat16(), torch.randn(T, d, device="cuda", generator=g).bfloat16()
+    y = first.forward(x, train=train)
+    grads = first.backward(dy) if train else {}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(100_000_000)  # some 50 ms of the current stream
+    y2 = again.forward(x, side, train=train)
+    grads2 = again.backward(dy, side) if train else {}
+    side.synchronize()
+    assert torch.equal(y2, y)
+    for name, v in grads.items():
+        assert v is None or torch.equal(grads2[name], v), name
+    assert N.get_device_error() == 0
