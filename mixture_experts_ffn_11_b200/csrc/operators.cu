@@ -172,6 +172,8 @@ struct NormShape {
     size_t smem;
 };
 constexpr size_t kNormRingBytes = 204 * 1024;
+// the widest row, of the gradient in front with an fp32 stream and dres, has a stage
+static_assert(BN_MAX_D * (2 + 4 + 4) <= kNormRingBytes - 256, "stages");
 NormShape norm_shape(int T, int d, int sms, size_t row_bytes, int vpt1_max, int per_sm, int most) {
     const int nvec = d / 8;
     NormShape s{};
@@ -187,10 +189,6 @@ NormShape norm_shape(int T, int d, int sms, size_t row_bytes, int vpt1_max, int 
     while (m > 1 && (m * s.threads > 1536 || 2 * row_bytes > kNormRingBytes / m)) --m;
     s.grid = m * sms < T ? m * sms : T;
     s.stages = (int)std::min<size_t>(BN_MAX_STAGES, (kNormRingBytes / m - 256) / row_bytes);
-    if (s.stages < 1) {  // rows too wide for a ring
-        s.stages = 0;
-        return s;
-    }
     s.smem = 128 + (size_t)s.stages * row_bytes;
     return s;
 }
