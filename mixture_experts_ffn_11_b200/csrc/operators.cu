@@ -8,6 +8,14 @@
 #include "fp8_quant.cuh"
 #include "gemm_fp8.cuh"
 
+namespace {
+// fp32 and int32 arrays (null ones are the caller's to allow)
+template <typename... P>
+bool aligned4(const P*... p) {
+    return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
+}  // namespace
+
 // ---- the whole layer for few tokens ----
 namespace {
 
@@ -141,8 +149,7 @@ moe_status_t gemm_fp8(const uint8_t* a, const float* sa, const uint8_t* w, const
     if (!w || !sw || !offsets || (M > 0 && (!a || !sa || !out))) return fail(MOE_ERR_INVALID_ARG, "null pointer argument");
     if (!aligned16(a) || !aligned16(w) || !aligned16(out))
         return fail(MOE_ERR_INVALID_ARG, "value and output pointers must be 16-byte aligned");
-    if (((reinterpret_cast<uintptr_t>(offsets) | reinterpret_cast<uintptr_t>(sa) | reinterpret_cast<uintptr_t>(sw)) & 3u) != 0)
-        return fail(MOE_ERR_INVALID_ARG, "offsets or scales misaligned");
+    if (!aligned4(offsets, sa, sw)) return fail(MOE_ERR_INVALID_ARG, "offsets or scales misaligned");
     if (G < 1 || G > GG_MAX_GROUPS) return fail(MOE_ERR_INVALID_ARG, "G=%d outside [1, %d]", G, GG_MAX_GROUPS);
     if (M < 0) return fail(MOE_ERR_INVALID_ARG, "M=%d < 0", M);
     if (d < 16 || f < 16 || d % 16 || f % 16)
@@ -457,6 +464,8 @@ moe_status_t moe_few_tokens(const moe_bf16_t* x, const float* w_router, const fl
     if (!aligned16(x) || !aligned16(w_router) || !aligned16(w_gateup) || !aligned16(w_down) || !aligned16(w_gateup_shared) ||
         !aligned16(w_down_shared) || !aligned16(y))
         return fail(MOE_ERR_INVALID_ARG, "x, y and weight pointers must be 16-byte aligned");
+    if (!aligned4(bias, logits_out, topk_idx, topk_w))
+        return fail(MOE_ERR_INVALID_ARG, "bias, logits_out, topk_idx and topk_w must be 4-byte aligned");
     const FewWorkspace w = few_workspace(T, d, f, fs, k);
     if (!ws || ws_bytes < w.bytes)
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", w.bytes, ws ? ws_bytes : (size_t)0);
@@ -501,7 +510,7 @@ moe_status_t moe_fp8_block_quantize(const moe_bf16_t* w, int G, int N, int K, ui
     if (K < 16 || K % 16) return fail(MOE_ERR_INVALID_ARG, "K=%d must be a positive multiple of 16", K);
     if (G == 0 || N == 0) return MOE_OK;
     if (!w || !q || !s) return fail(MOE_ERR_INVALID_ARG, "null pointer");
-    if (!aligned16(w) || !aligned16(q) || (reinterpret_cast<uintptr_t>(s) & 3u) != 0)
+    if (!aligned16(w) || !aligned16(q) || !aligned4(s))
         return fail(MOE_ERR_INVALID_ARG, "w and q must be 16-byte, s 4-byte aligned");
     DeviceInfo di;
     moe_status_t st = operator_device(di);
@@ -519,8 +528,7 @@ moe_status_t moe_fp8_row_quantize(const moe_bf16_t* x, const int32_t* row_src, i
     if (!row_src && R > T) return fail(MOE_ERR_INVALID_ARG, "R=%d rows of T=%d without row_src", R, T);
     if (R == 0) return MOE_OK;
     if (T == 0 || !x || !q || !s) return fail(MOE_ERR_INVALID_ARG, "no source rows, or null pointer");
-    if (!aligned16(x) || !aligned16(q) ||
-        ((reinterpret_cast<uintptr_t>(row_src) | reinterpret_cast<uintptr_t>(s)) & 3u) != 0)
+    if (!aligned16(x) || !aligned16(q) || !aligned4(row_src, s))
         return fail(MOE_ERR_INVALID_ARG, "x and q must be 16-byte, row_src and s 4-byte aligned");
     DeviceInfo di;
     moe_status_t st = operator_device(di);
@@ -556,6 +564,7 @@ moe_status_t moe_block_norm_in(const void* x, moe_stream_type_t type, const floa
     if (st != MOE_OK) return st;
     if (!w || (T > 0 && (!x || !xn || !rstd))) return fail(MOE_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(x) || !aligned16(w) || !aligned16(xn)) return fail(MOE_ERR_INVALID_ARG, "x, w and xn must be 16-byte aligned");
+    if (!aligned4(rstd)) return fail(MOE_ERR_INVALID_ARG, "rstd must be 4-byte aligned");
     DeviceInfo di;
     if ((st = norm_device(di)) != MOE_OK) return st;
     if (T == 0) return MOE_OK;
@@ -576,6 +585,7 @@ moe_status_t moe_block_norm_out(const moe_bf16_t* y, const void* r, moe_stream_t
     if (!aligned16(y) || !aligned16(r) || !aligned16(w) || !aligned16(gate) || !aligned16(w_next) || !aligned16(out) ||
         !aligned16(xn))
         return fail(MOE_ERR_INVALID_ARG, "y, r, w, gate, w_next, out and xn must be 16-byte aligned");
+    if (!aligned4(rstd, rstd_next)) return fail(MOE_ERR_INVALID_ARG, "rstd and rstd_next must be 4-byte aligned");
     DeviceInfo di;
     if ((st = norm_device(di)) != MOE_OK) return st;
     if (T == 0) return MOE_OK;
@@ -603,6 +613,7 @@ moe_status_t moe_block_norm_in_backward(const moe_bf16_t* dxn, const void* dres,
     if (!w || !dw || (T > 0 && (!dxn || !x || !rstd || !dx))) return fail(MOE_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(dxn) || !aligned16(dres) || !aligned16(x) || !aligned16(w) || !aligned16(dx))
         return fail(MOE_ERR_INVALID_ARG, "dxn, dres, x, w and dx must be 16-byte aligned");
+    if (!aligned4(rstd, dw)) return fail(MOE_ERR_INVALID_ARG, "rstd and dw must be 4-byte aligned");
     const size_t need = T > 0 ? norm_grad_ws(T, d, 0) : 0;
     if (need && (!ws || ws_bytes < need))
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
@@ -640,6 +651,8 @@ moe_status_t moe_block_norm_out_backward(const void* dout, const moe_bf16_t* dxn
     if (!aligned16(dout) || !aligned16(dxn) || !aligned16(y) || !aligned16(out) || !aligned16(w) || !aligned16(gate) ||
         !aligned16(w_next) || !aligned16(dr) || !aligned16(dy) || !aligned16(dgate))
         return fail(MOE_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+    if (!aligned4(rstd, rstd_next, dw, dw_next))
+        return fail(MOE_ERR_INVALID_ARG, "rstd, rstd_next, dw and dw_next must be 4-byte aligned");
     const size_t need = T > 0 ? norm_grad_ws(T, d, gate_rows) : 0;
     if (need && (!ws || ws_bytes < need))
         return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
