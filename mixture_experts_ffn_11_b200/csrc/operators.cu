@@ -140,9 +140,13 @@ moe_status_t launch_fp8(const uint8_t* a, const float* sa, const uint8_t* w, con
 // more ring stages, wide ones read a group's weights fewer times. Which is decided by the average rows per group, the only
 // thing the host knows of the groups. Measured, groups within half of the average either way, gate|up / down in us:
 //   32 groups, d = f = 2880       average 32: 64 rows 87 / 52, 128 rows 88 / 53      48: 64 rows 108 / 60, 128 rows 94 / 54
-//                                 average 112: 128 rows 136 / 70, 256 rows 143 / 83  128: 128 rows 153 / 79, 256 rows 146 / 78
-//   128 groups, d 2048, f 768     average 96: 128 rows 104 / 68, 256 rows 117 / 71   128: 128 rows 123 / 80, 256 rows 126 / 75
-//   8 groups, d 4096, f 14336     average 96: 128 rows 193 / 92, 256 rows 220 / 112  128: 128 rows 275 / 133, 256 rows 245 / 118
+//                                 average 96: 128 rows 123 / 67, 256 rows 137 / 75   112: 128 rows 136 / 70, 256 rows 143 / 83
+//                                 average 128: 128 rows 153 / 79, 256 rows 146 / 78
+//   128 groups, d 2048, f 768     average 96: 128 rows 104 / 68, 256 rows 117 / 71   112: 128 rows 115 / 76, 256 rows 116 / 72
+//                                 average 128: 128 rows 123 / 80, 256 rows 126 / 75
+//   8 groups, d 4096, f 14336     average 96: 128 rows 193 / 92, 256 rows 220 / 112  112: 128 rows 231 / 133, 256 rows 235 / 115
+//                                 average 128: 128 rows 275 / 133, 256 rows 245 / 118
+// At 112 both products together are 20 us apart for 32 groups (128 rows the faster), 3 and 15 the other way for 128 and 8: 112 takes 128.
 template <bool GATEUP>
 moe_status_t gemm_fp8(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, const int32_t* offsets, int G, int M,
                       int d, int f, moe_bf16_t* out, cudaStream_t stream) {
