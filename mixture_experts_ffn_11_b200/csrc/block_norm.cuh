@@ -16,7 +16,7 @@
 //
 // Measured (HBM's floor at a copy's rate in brackets): behind the block with the next norm, 4096 rows of 2880 in bf16, 25 us (14.4; its
 // output mostly stays in L2, a row's reductions and stores set the pace); its gradient with a gate, 8192 rows of 4096 with an fp32 stream,
-// 109 us (92), in bf16 89 us (62); the gradient in front, 4096 rows of 2880, 25.5 us (14.4), in two kernels, the second, launched ahead,
+// 107 us (92), in bf16 88 us (62); the gradient in front, 4096 rows of 2880, 25 us (14.4), in two kernels, the second, launched ahead,
 // adding the CTAs' partial sums in a fixed order, four rows of them at a time (launched behind the first 30.4 us); in front, 64 rows of
 // 7168, 1.9 us (0.3), a launch. Rows by plain loads, one thread for all of a row's columns: 28.9, 238, -, 42.3.
 #pragma once
@@ -619,8 +619,8 @@ struct NormOutGradArgs {
 //
 // A thread keeps one vector of 8 columns: gains, sums and a row's values are up to 80 registers for it. Rows of more columns than
 // a CTA's threads hold are cut over the CTAs of a cluster. (With two or four vectors per thread they spilled: 4096 rows of 8192 in
-// bf16 202 us instead of 132, 2048 of 16384 in fp32 921 us instead of 155.) Instructions and the steps from row to row bound it there, HBM
-// for one CTA per row in fp32 (8192 rows of 4096 with gate and next norm: 109 us, floor 92; bf16 89 us, floor 62).
+// bf16 202 us instead of 137, 2048 of 16384 in fp32 921 us instead of 151.) Instructions and the steps from row to row bound it there, HBM
+// for one CTA per row in fp32 (8192 rows of 4096 with gate and next norm: 107 us, floor 92; bf16 88 us, floor 62).
 template <typename R, bool NEXT, bool GATE, bool RING, bool CLUSTER>
 __global__ void __launch_bounds__(BN_MAX_THREADS) block_norm_out_grad_kernel(const NormOutGradArgs a, int stages) {
     extern __shared__ __align__(128) uint8_t smem[];
