@@ -520,9 +520,11 @@ moe_status_t moe_fp8_block_quantize(const moe_bf16_t* w, int G, int N, int K, ui
     moe_status_t st = operator_device(di);
     if (st != MOE_OK) return st;
     const long blocks = (long)G * ((N + F8_BLOCK - 1) / F8_BLOCK) * ((K + F8_BLOCK - 1) / F8_BLOCK);
+    // Both encoders are launched plainly: between two expert products they are elementwise kernels behind a GEMM and in front of a
+    // CTA-pair GEMM, the place in which one that was launched early stalled the stream (launch_plain).
     return check_launch("fp8_block_quantize",
-                        launch_pdl(fp8_block_quantize_kernel, dim3(grid_cap(blocks, di.sms, 6)), dim3(256), 0, stream,
-                                   reinterpret_cast<const __nv_bfloat16*>(w), N, K, blocks, q, s));
+                        launch_plain(fp8_block_quantize_kernel, dim3(grid_cap(blocks, di.sms, 6)), dim3(256), 0, stream,
+                                     reinterpret_cast<const __nv_bfloat16*>(w), N, K, blocks, q, s));
 }
 
 moe_status_t moe_fp8_row_quantize(const moe_bf16_t* x, const int32_t* row_src, int T, int K, int R, uint8_t* q, float* s,
@@ -540,8 +542,7 @@ moe_status_t moe_fp8_row_quantize(const moe_bf16_t* x, const int32_t* row_src, i
     const int chunks = (K / 8 + F8_CHUNK_VEC - 1) / F8_CHUNK_VEC;
     if (chunks > 65535) return fail(MOE_ERR_INVALID_ARG, "K=%d too large", K);
     const int grid = grid_cap(((long)R + 7) / 8, std::max(1, di.sms / chunks), 6);
-    // Launched plainly: between the two expert products it is an elementwise kernel behind a GEMM and in front of a CTA-pair GEMM, the
-    // place in which one that was launched early stalled the stream (launch_plain).
+    // (plainly: see moe_fp8_block_quantize)
     return check_launch("fp8_row_quantize",
                         launch_plain(fp8_row_quantize_kernel, dim3(grid, chunks), dim3(256), 0, stream,
                                      reinterpret_cast<const __nv_bfloat16*>(x), row_src, T, K, R, q, s));

@@ -54,3 +54,19 @@ def test_the_encoder_between_the_fp8_products():
     early = launched_early(lambda: (products(), products()))
     assert early[1::2] == [False] * 3  # the encoders
     assert early[2::2] == [True] * 3   # the products behind them
+
+
+def test_the_weight_encoder_between_the_fp8_products():
+    M, G, d = 40, 2, 128
+    new = lambda *s, t=N.E4M3: torch.empty(s, dtype=t, device="cuda")  # noqa: E731
+    f32, bf = torch.float32, torch.bfloat16
+    off = torch.tensor([0, 30, M], dtype=torch.int32, device="cuda")
+    w, wq, ws, xq, xs, y = new(G, d, d, t=bf), new(G, d, d), new(G, 1, 1, t=f32), new(M, d), new(1, M, t=f32), new(M, d, t=bf)
+
+    def product():
+        N.fp8_block_quantize(w, wq, ws)
+        N.grouped_gemm_down_fp8(xq, xs, wq, ws, off, y)
+
+    early = launched_early(lambda: (product(), product(), product()))
+    assert early[1::2] == [False] * 2
+    assert early[2::2] == [True] * 2
