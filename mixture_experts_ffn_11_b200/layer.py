@@ -50,10 +50,13 @@ def _encode_fp8(w, halves: int):
     return q, s
 
 
-def _in_use(buffers: dict, stream, seen: set):
+def _in_use(buffers: dict, stream, seen: set, captured: dict, key):
     """Tell the caching allocator that `stream` uses these buffers, which were allocated on whichever stream was current: when they are
     dropped (for another number of tokens), their memory is not given out while that stream's work is still to come. `seen`: streams
-    it has been told of."""
+    it has been told of. While a CUDA graph is captured they are entered in `captured` under their key and never dropped: the graph's
+    replays write them."""
+    if torch.cuda.is_current_stream_capturing():
+        captured[key] = (buffers, seen)
     if stream.cuda_stream in seen:
         return
     seen.add(stream.cuda_stream)
@@ -145,6 +148,7 @@ class MoEFFN:
             self.w_gateup = self.w_down = self.w_gateup_shared = self.w_down_shared = None
         self._T = None
         self.buf = {}
+        self._captured, self._gcaptured = {}, {}  # buffers that CUDA graphs were captured with, by T
         # the tensor-core router (E <= 128) reads W_r as three bf16 pieces: split once here, not in every call
         self.w_pieces = None
         if self.E <= 128:
@@ -159,6 +163,7 @@ class MoEFFN:
         and side stream, so that two calls can be in flight at once."""
         twin = copy.copy(self)
         twin.buf, twin._T = {}, None
+        twin._captured, twin._gcaptured = {}, {}
         twin._gbuf, twin._gT, twin._gu_saved = None, None, False  # its own backward buffers too
         twin._side = torch.cuda.Stream(self.device) if self.shared_f else None
         return twin
@@ -169,8 +174,12 @@ class MoEFFN:
             N.router_split_weights(self.w_router, self.w_pieces)
 
     def buffers(self, T: int) -> dict:
-        """Allocate (once per T) every intermediate the layer writes."""
+        """Every intermediate the layer writes, for T tokens: those of the last call, or of a CUDA graph captured with T tokens, else
+        new ones."""
         if self._T == T:
+            return self.buf
+        if T in self._captured:
+            (self.buf, self._seen), self._T = self._captured[T], T
             return self.buf
         dev, E, d, f, k = self.device, self.E, self.d, self.f, self.k
         R = T * k
@@ -241,8 +250,8 @@ class MoEFFN:
         if few and "few_ws" not in b:
             n = N.few_tokens_workspace_size(T, self.d, self.f, self.shared_f, self.E, self.k)
             b["few_ws"] = torch.empty(n, dtype=torch.uint8, device=self.device)
-            self._seen = set()
-        _in_use(b, s, self._seen)
+            self._seen.clear()
+        _in_use(b, s, self._seen, self._captured, T)
         self._x = x  # the backward pass reads the forward's input and intermediates
 
         def mark(name, first):
@@ -310,7 +319,7 @@ class MoEFFN:
             N.grouped_gemm_gateup_gather(x, b["perm_src"], self.w_gateup, b["offsets"], b["h"], None, s)
         elif save:
             g = self._made_on(s, getattr(self, "_gT", None) == T, self._grad_buffers, T)
-            _in_use(g, s, self._gseen)
+            _in_use(g, s, self._gseen, self._gcaptured, T)
             N.grouped_gemm_gateup_save(b["x_perm"], self.w_gateup, b["offsets"], b["h"], g["gu"], s)
             self._gu_saved = True
         else:
@@ -419,6 +428,9 @@ class MoEFFN:
     def _grad_buffers(self, T: int) -> dict:
         if getattr(self, "_gT", None) == T:
             return self._gbuf
+        if T in self._gcaptured:
+            (self._gbuf, self._gseen), self._gT = self._gcaptured[T], T
+            return self._gbuf
         dev, E, d, f, k = self.device, self.E, self.d, self.f, self.k
         R = T * k
         bf, f32 = torch.bfloat16, torch.float32
@@ -463,8 +475,8 @@ class MoEFFN:
         b = self.buf
         wt = self._made_on(s, getattr(self, "_wt", None) is not None, self._transposed)
         g = self._made_on(s, getattr(self, "_gT", None) == T, self._grad_buffers, T)
-        _in_use(b, s, self._seen)
-        _in_use(g, s, self._gseen)
+        _in_use(b, s, self._seen, self._captured, T)
+        _in_use(g, s, self._gseen, self._gcaptured, T)
         x = self._x
 
         def mark(name, first):
@@ -582,15 +594,22 @@ class MoEBlock:
             raise ValueError(f"w_in, w_out and gate are vectors of d = {ffn.d}")
         self.ffn, self.w_in, self.w_out, self.gate, self.alpha, self.eps = ffn, w_in, w_out, gate, alpha, eps
         self._key, self._buf, self._call = None, {}, None
+        self._gkey, self._gbuf = None, {}
+        self._captured, self._gcaptured = {}, {}  # buffers that CUDA graphs were captured with
 
     def _buffers(self, T: int, dtype) -> dict:
-        """Outputs and kept values, allocated once per T and type of the stream."""
-        if self._key != (T, dtype):
+        """Outputs and kept values for T tokens and this type of the stream, kept as MoEFFN.buffers() keeps its own."""
+        if self._key == (T, dtype):
+            return self._buf
+        if (T, dtype) in self._captured:
+            self._buf, self._seen = self._captured[T, dtype]
+        else:
             d, dev = self.ffn.d, self.ffn.device
             new = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=dev)  # noqa: E731
             self._buf = {"xn": new(T, d, t=torch.bfloat16), "rstd_in": new(T), "out": new(T, d, t=dtype), "rstd": new(T),
                          "xn_next": new(T, d, t=torch.bfloat16), "rstd_next": new(T)}
-            self._key, self._seen = (T, dtype), set()
+            self._seen = set()
+        self._key = (T, dtype)
         return self._buf
 
     def forward(self, r, xn=None, next_norm=None, gate=None, gate_rows: int = 0, train: bool = False, stream=None):
@@ -602,7 +621,7 @@ class MoEBlock:
         self._call = None  # whatever becomes of this call, the kept values of the one before are gone
         b = self._buffers(T, r.dtype)
         stream = stream if stream is not None else torch.cuda.current_stream(self.ffn.device)
-        _in_use(b, stream, self._seen)
+        _in_use(b, stream, self._seen, self._captured, self._key)
         if T > 0:
             store = lambda t: t.untyped_storage().data_ptr()  # noqa: E731
             reads = {store(t) for t in ((r, xn) if train else (r,)) if t is not None}
@@ -642,7 +661,9 @@ class MoEBlock:
                                "beside them, need a MoEFFN of their own: sibling() gives one over the same weights)")
         T, d = r.shape
         key = (T, r.dtype, gate_rows)
-        if getattr(self, "_gkey", None) != key:
+        if self._gkey != key and key in self._gcaptured:
+            (self._gbuf, self._gseen), self._gkey = self._gcaptured[key], key
+        if self._gkey != key:
             new = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device=f.device)  # noqa: E731
             ws = N.block_norm_backward_workspace_size(T, d, gate_rows)
             self._gbuf = {"dr": new(T, d, t=r.dtype), "dy": new(T, d, t=torch.bfloat16), "dw_out": new(d), "dw_in": new(d),
@@ -651,8 +672,8 @@ class MoEBlock:
             self._gkey, self._gseen = key, set()
         g = self._gbuf
         stream = stream if stream is not None else torch.cuda.current_stream(f.device)
-        _in_use(b, stream, self._seen)
-        _in_use(g, stream, self._gseen)
+        _in_use(b, stream, self._seen, self._captured, self._key)
+        _in_use(g, stream, self._gseen, self._gcaptured, key)
         nxt = next_norm is not None
         N.block_norm_out_backward(dout, dxn, y, b["out"] if nxt else None, self.w_out, gate, gate_rows, self.alpha, next_norm,
                                   b["rstd"], b["rstd_next"] if nxt else None, g["dr"], g["dy"], g["dw_out"], g["dgate"],

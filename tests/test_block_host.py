@@ -1,5 +1,8 @@
 """MoEBlock's checks on the host, on the CPU with a stand-in for the layer and the norms: calls whose inputs it would overwrite before it, or
 its backward pass, has read them, and backward passes whose kept values are gone."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -12,6 +15,7 @@ class Stream:
 def block(monkeypatch):
     from mixture_experts_ffn_11_b200 import MoEBlock, layer
 
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
     refuse = []
 
@@ -93,3 +97,24 @@ def test_a_refused_forward_leaves_nothing_to_go_back_to(block):
         block.forward(r, train=True, stream=Stream)
     with pytest.raises(RuntimeError):
         block.backward(dout, stream=Stream)
+
+
+def test_buffers_of_a_captured_call_are_kept(block, monkeypatch):
+    r = torch.zeros(4, 16)
+    capturing = [True]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    block.forward(r, train=True, stream=Stream)
+    block.backward(r, stream=Stream)
+    held = [weakref.ref(t) for b in (block._buf, block._gbuf) for t in b.values() if t is not None]
+    at = block._buf["out"].data_ptr(), block._gbuf["dr"].data_ptr()
+    capturing[0] = False
+    block.forward(torch.zeros(5, 16), train=True, stream=Stream)
+    block.backward(torch.zeros(5, 16), stream=Stream)
+    dropped = [weakref.ref(t) for b in (block._buf, block._gbuf) for t in b.values() if t is not None]
+    block.forward(torch.zeros(6, 16), train=True, stream=Stream)
+    block.backward(torch.zeros(6, 16), stream=Stream)
+    gc.collect()
+    assert all(h() is not None for h in held) and all(h() is None for h in dropped)
+    block.forward(r, train=True, stream=Stream)  # the same tokens again: the same buffers
+    block.backward(r, stream=Stream)
+    assert at == (block._buf["out"].data_ptr(), block._gbuf["dr"].data_ptr())

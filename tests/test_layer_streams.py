@@ -14,6 +14,7 @@ def test_block_buffers_are_recorded_on_every_stream_once(monkeypatch):
     from mixture_experts_ffn_11_b200 import layer
 
     told = []
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: told.append((t.data_ptr(), s.cuda_stream)))
     for name in ("block_norm_in", "block_norm_out", "block_norm_in_backward", "block_norm_out_backward"):
         monkeypatch.setattr(layer.N, name, lambda *a: None)
@@ -109,4 +110,58 @@ def test_first_call_on_a_side_stream_beside_a_busy_current_one(weights, fs):
     assert torch.equal(y2, y)
     for name, v in grads.items():
         assert v is None or torch.equal(grads2[name], v), name
+    assert N.get_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("few,weights,fs", [(False, "bf16", 128), (True, "bf16", 0), (False, "mxfp4", 256), (False, "fp8", 128)])
+def test_graphs_of_several_numbers_of_tokens(few, weights, fs):
+    """One graph per number of tokens of a block, forward (with bf16 weights and the backward pass), the usual way: a call to warm up, then the
+    capture. The graphs are replayed in any order between calls for other numbers of tokens, and nothing of them is written elsewhere."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mixture_experts_ffn_11_b200 import MoEBlock, MoEFFN
+    from mixture_experts_ffn_11_b200 import _native as N
+
+    torch.cuda.set_device(0)
+    E, d, f, k = 16, 256, 256, 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=g) * 0.05  # noqa: E731
+    args = (n(E, d), n(E, 2 * f, d).bfloat16(), n(E, d, f).bfloat16(), k, "topk_softmax", None,
+            n(2 * fs, d).bfloat16() if fs else None, n(d, fs).bfloat16() if fs else None)
+    train = weights == "bf16" and not few
+    gains = 1 + n(d), 1 + n(d)
+    block = MoEBlock(MoEFFN(*args, weights=weights, few=few), *gains)
+    plain = MoEBlock(MoEFFN(*args, weights=weights, few=few), *gains)
+
+    def step(b, r):
+        out = b(r, train=train)
+        got = {"out": out}
+        if train:
+            got.update({m: v for m, v in b.backward(torch.ones_like(r)).items() if v is not None})
+        return got
+
+    graphs = []
+    for T in (4, 12, 40):
+        r = torch.randn(T, d, device="cuda", generator=g)
+        step(block, r)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step(block, r)
+        graphs.append((graph, r, got))
+    torch.cuda.empty_cache()
+    block(torch.randn(7, d, device="cuda"))
+    others = [torch.full((m, c), 7.0, dtype=t, device="cuda") for _ in range(6) for m in (4, 8, 12, 24, 40, 80) for c in (1, d, f, 2 * f)
+              for t in (torch.bfloat16, torch.float32)]
+    for graph, r, got in graphs + graphs[::-1]:
+        r.copy_(torch.randn(r.shape, device="cuda", generator=g))
+        block(torch.randn(9, d, device="cuda"))
+        graph.replay()
+        want = step(plain, r)
+        for name, v in want.items():
+            assert torch.equal(got[name], v), name
+        twice = step(block, r)  # the same number of tokens without the graph
+        assert torch.equal(twice["out"], want["out"])
+    assert all(bool((o == 7).all()) for o in others)
     assert N.get_device_error() == 0
