@@ -232,6 +232,12 @@ class MoEFFN:
         with torch.cuda.stream(stream):
             return make(*args)
 
+    def output_there(self, T: int):
+        """The output buffer that forward() will write for T tokens, if it is there already, else None."""
+        if self._T == T:
+            return self.buf["y"]
+        return self._captured[T][0]["y"] if T in self._captured else None
+
     def forward(self, x, stream=None, timing=None, train: bool = False):
         """y = MoE(x) for x [T, d] bf16 on the GPU. Returns the layer's output buffer [T, d] (bf16).
 
@@ -584,7 +590,8 @@ class MoEBlock:
 
         out = alpha * r + gate * (w_out * norm(ffn(w_in * norm(r)))),  norm(v) = v / sqrt(mean(v^2) + eps)
 
-    ffn: the MoEFFN; w_in, w_out [d] fp32 gains; gate: None, or a learned gate [d] bf16 (forward() also takes one per call); alpha
+    ffn: the MoEFFN (one to a block while training: backward() reads its intermediates; MoEFFN.sibling() gives another over the same
+    weights); w_in, w_out [d] fp32 gains; gate: None, or a learned gate [d] bf16 (forward() also takes one per call); alpha
     the residual scale. The residual stream r is bf16 or fp32 [T, d]. Blocks in a row pass the next one's normed input on, made in
     the same pass as the residual: out, xn = a(r, next_norm=b.w_in); out = b(out, xn=xn).
     """
@@ -625,7 +632,7 @@ class MoEBlock:
         if T > 0:
             store = lambda t: t.untyped_storage().data_ptr()  # noqa: E731
             reads = {store(t) for t in ((r, xn) if train else (r,)) if t is not None}
-            y = getattr(self.ffn, "buf", {}).get("y")
+            y = self.ffn.output_there(T)
             if y is not None and store(y) in reads:
                 raise ValueError("r (and xn, with train) may not be the MoEFFN's own output: its forward() overwrites that before it is read")
             if train and reads & {store(t) for t in (b["out"], b["xn_next"] if next_norm is not None else b["out"])}:

@@ -36,6 +36,9 @@ def block(monkeypatch):
                 self.buf = {"y": torch.zeros(x.shape, dtype=torch.bfloat16)}
             return self.buf["y"]
 
+        def output_there(self, T):
+            return self.buf["y"] if self.buf and self.buf["y"].shape[0] == T else None
+
         def backward(self, dy, weight_grads=True, stream=None):
             return {"dx": torch.zeros_like(dy)}
 
@@ -69,6 +72,16 @@ def test_the_layers_output_is_refused_as_the_stream(block):
         block.forward(r, xn=y, train=True, stream=Stream)
     block.forward(r, xn=y, stream=Stream)
     block.forward(y.clone(), train=True, stream=Stream)
+    block.forward(y[:2], stream=Stream)  # another number of tokens: the layer writes another buffer
+
+
+def test_the_output_that_the_layer_will_write():
+    from mixture_experts_ffn_11_b200 import MoEFFN
+
+    lay = object.__new__(MoEFFN)
+    y4, y8 = torch.zeros(4, 16), torch.zeros(8, 16)
+    lay._T, lay.buf, lay._captured = 8, {"y": y8}, {4: ({"y": y4}, set())}
+    assert lay.output_there(8) is y8 and lay.output_there(4) is y4 and lay.output_there(5) is None
 
 
 def test_backward_after_another_forward_of_the_layer(block):
