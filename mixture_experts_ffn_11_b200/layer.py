@@ -50,20 +50,28 @@ def _encode_fp8(w, halves: int):
     return q, s
 
 
-def _in_use(buffers: dict, stream, seen: set, captured: dict, key):
-    """Tell the caching allocator that `stream` uses these buffers, which were allocated on whichever stream was current: when they are
+def _in_use(buffers: dict, stream, device, seen: set, captured: dict, key):
+    """Tell the caching allocator that `stream` (None: the device's current one) uses these buffers, which were allocated on whichever stream was current: when they are
     dropped (for another number of tokens), their memory is not given out while that stream's work is still to come. `seen`: streams
     it has been told of. While a CUDA graph is captured they are entered in `captured` under their key and never dropped: the graph's
     replays write them."""
-    if torch.cuda.is_current_stream_capturing():
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    if raw != 0 and torch.cuda.is_current_stream_capturing():  # (the default stream cannot be captured)
         captured[key] = (buffers, seen)
-    if stream.cuda_stream in seen:
+    if raw in seen:
         return
-    seen.add(stream.cuda_stream)
+    seen.add(raw)
+    stream = stream if stream is not None else torch.cuda.current_stream(device)
     for v in buffers.values():
         for t in v if isinstance(v, tuple) else (v,):  # (encoded rows: values and scales)
             if t is not None:
                 t.record_stream(stream)
+
+
+def _overlap(a, b) -> bool:
+    """Whether two contiguous tensors share memory."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    return a0 < b0 + b.nbytes and b0 < a0 + a.nbytes
 
 
 class MoEFFN:
@@ -257,7 +265,7 @@ class MoEFFN:
             n = N.few_tokens_workspace_size(T, self.d, self.f, self.shared_f, self.E, self.k)
             b["few_ws"] = torch.empty(n, dtype=torch.uint8, device=self.device)
             self._seen.clear()
-        _in_use(b, s, self._seen, self._captured, T)
+        _in_use(b, s, self.device, self._seen, self._captured, T)
         self._x = x  # the backward pass reads the forward's input and intermediates
 
         def mark(name, first):
@@ -325,7 +333,7 @@ class MoEFFN:
             N.grouped_gemm_gateup_gather(x, b["perm_src"], self.w_gateup, b["offsets"], b["h"], None, s)
         elif save:
             g = self._made_on(s, getattr(self, "_gT", None) == T, self._grad_buffers, T)
-            _in_use(g, s, self._gseen, self._gcaptured, T)
+            _in_use(g, s, self.device, self._gseen, self._gcaptured, T)
             N.grouped_gemm_gateup_save(b["x_perm"], self.w_gateup, b["offsets"], b["h"], g["gu"], s)
             self._gu_saved = True
         else:
@@ -481,8 +489,8 @@ class MoEFFN:
         b = self.buf
         wt = self._made_on(s, getattr(self, "_wt", None) is not None, self._transposed)
         g = self._made_on(s, getattr(self, "_gT", None) == T, self._grad_buffers, T)
-        _in_use(b, s, self._seen, self._captured, T)
-        _in_use(g, s, self._gseen, self._gcaptured, T)
+        _in_use(b, s, self.device, self._seen, self._captured, T)
+        _in_use(g, s, self.device, self._gseen, self._gcaptured, T)
         x = self._x
 
         def mark(name, first):
@@ -627,15 +635,13 @@ class MoEBlock:
         T = r.shape[0]
         self._call = None  # whatever becomes of this call, the kept values of the one before are gone
         b = self._buffers(T, r.dtype)
-        stream = stream if stream is not None else torch.cuda.current_stream(self.ffn.device)
-        _in_use(b, stream, self._seen, self._captured, self._key)
+        _in_use(b, stream, self.ffn.device, self._seen, self._captured, self._key)
         if T > 0:
-            store = lambda t: t.untyped_storage().data_ptr()  # noqa: E731
-            reads = {store(t) for t in ((r, xn) if train else (r,)) if t is not None}
+            reads = (r,) if xn is None or not train else (r, xn)
             y = self.ffn.output_there(T)
-            if y is not None and store(y) in reads:
+            if y is not None and any(_overlap(t, y) for t in reads):
                 raise ValueError("r (and xn, with train) may not be the MoEFFN's own output: its forward() overwrites that before it is read")
-            if train and reads & {store(t) for t in (b["out"], b["xn_next"] if next_norm is not None else b["out"])}:
+            if train and any(_overlap(t, b["out"]) or (next_norm is not None and _overlap(t, b["xn_next"])) for t in reads):
                 raise ValueError("backward() reads r and xn, and this forward would overwrite them: they are the block's own outputs")
         if gate is None and self.gate is not None:
             gate, gate_rows = self.gate.view(1, -1)[:min(T, 1)], max(T, 1)
@@ -678,9 +684,8 @@ class MoEBlock:
                           "ws": new(max(ws, 16), t=torch.uint8)}
             self._gkey, self._gseen = key, set()
         g = self._gbuf
-        stream = stream if stream is not None else torch.cuda.current_stream(f.device)
-        _in_use(b, stream, self._seen, self._captured, self._key)
-        _in_use(g, stream, self._gseen, self._gcaptured, key)
+        _in_use(b, stream, f.device, self._seen, self._captured, self._key)
+        _in_use(g, stream, f.device, self._gseen, self._gcaptured, key)
         nxt = next_norm is not None
         N.block_norm_out_backward(dout, dxn, y, b["out"] if nxt else None, self.w_out, gate, gate_rows, self.alpha, next_norm,
                                   b["rstd"], b["rstd_next"] if nxt else None, g["dr"], g["dy"], g["dw_out"], g["dgate"],
